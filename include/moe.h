@@ -389,6 +389,105 @@ moe_status_t moe_fused(const moe_problem_t* problem, const moe_act_t* act,
 moe_status_t moe_permute_noalloc(const moe_problem_t* problem, const int64_t* topk_idx,
                                  const moe_layout_t* layout, int32_t* device_status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators next to the layer: what turns the residual stream into the
+ * layer's activations and router logits, and dense products in 8-bit
+ * integers.  All on one GPU, all enqueued on `stream`, none with a workspace.
+ * ------------------------------------------------------------------------- */
+
+/* Output encodings of moe_rmsnorm_quantize: the activation encodings of the
+ * layer's formats (same values as moe_format_t; NVFP4 activations come from
+ * MOE_NORM_BF16 and moe_quantize_nvfp4_rowwise), and 8-bit integers with one
+ * scale per token for moe_matmul_int8. */
+typedef enum {
+  MOE_NORM_BF16 = 0,
+  MOE_NORM_FP8_E4M3_B128 = 1,
+  MOE_NORM_MXFP8 = 3,
+  MOE_NORM_FP8_PER_TENSOR = 4,
+  MOE_NORM_INT8_PER_TOKEN = 5
+} moe_norm_format_t;
+
+/* Strides are in elements from one token to the next, 0 meaning hidden; they
+ * are at least hidden and a multiple of 16 bytes. */
+typedef struct {
+  int64_t num_tokens;          /* M >= 0 */
+  int64_t x_stride;
+  int64_t residual_in_stride;
+  int64_t residual_out_stride;
+  int32_t hidden;              /* H, multiple of 256, at most 32768 */
+  int32_t format;              /* moe_norm_format_t */
+  int32_t residual_fp32;       /* 0: the residual stream is BF16, 1: FP32 */
+  int32_t weight_fp32;         /* 0: the norm's weight is BF16, 1: FP32 */
+  float eps;                   /* finite, > 0 */
+} moe_norm_t;
+
+/* Residual addition, root-mean-square norm and activation encoding in one
+ * pass.  x is BF16 [M, H], residual_in and residual_out BF16 or FP32 [M, H]
+ * (residual_in may be NULL; residual_out may be NULL, or residual_in itself
+ * with the same stride), weight [H].  Per token, in FP32:
+ *   h = x + residual_in,  residual_out = round(h),
+ *   y = (h * rstd) * weight,  rstd = 1 / sqrt(sum(h^2) / H + eps)
+ * (the unrounded h is normalised), and y, rounded once,
+ *   to BF16 in norm_out [M, H] (may be NULL unless the format is BF16), and
+ *   to codes [M, H] with scales as the format says:
+ *     FP8_E4M3_B128    per 128 columns s = amax / 448, q = e4m3(y * (1/s));
+ *                      scales fp32 [M, H/128]
+ *     MXFP8            per 32 columns X = floor(log2 amax) - 8 clamped to
+ *                      [-127, 127] (-127 where amax = 0), q = e4m3(y * 2^-X);
+ *                      scales ue8m0 [M, H/32] = X + 127
+ *     FP8_PER_TENSOR   q = e4m3(y * (1/static_scale)); static_scale fp32 [1]
+ *                      on the device, a positive normal number (anything else
+ *                      gives NaN codes); scales NULL
+ *     INT8_PER_TOKEN   per token s = amax / 127, q = rint(y * (1/s)) in
+ *                      [-127, 127]; scales fp32 [M]
+ *     BF16             codes and scales NULL
+ * static_scale is NULL in every other format.  E4M3 saturates at 448.  Where
+ * a quotient s is below 2^-126 (a block of zeros), s and its codes are 0.
+ * A token whose sum of squares is not finite gives NaN throughout, a block
+ * whose amax is not finite NaN in the block: scales NaN (MXFP8: 255), E4M3
+ * codes NaN, integer codes 0.  Every pointer is 16-byte aligned, FP32 scales
+ * 4-byte; outputs overlap neither inputs nor one another
+ * (MOE_ERR_INVALID_ARG). */
+moe_status_t moe_rmsnorm_quantize(const moe_norm_t* problem, const void* x, const void* residual_in,
+                                  const void* weight, const float* static_scale, void* residual_out,
+                                  void* norm_out, void* codes, void* scales, void* stream);
+
+/* Router logits fp32 [M, E] = x . router_weight^T, as moe_route and moe_fused
+ * take them: x BF16 [M, H] (moe_rmsnorm_quantize's norm_out) and
+ * router_weight BF16 [E, H], both contiguous and 16-byte aligned; products
+ * and sums FP32.  Uses problem->num_tokens, ->hidden and ->num_experts (a
+ * fused shared expert has no logit).  device_status is one device int32 that
+ * the caller has set to MOE_OK and that the call sets to MOE_ERR_TIMEOUT if a
+ * bounded wait gives up (the outputs are then unspecified); the workspace's
+ * first word, its sticky status, serves. */
+moe_status_t moe_router_logits(const moe_problem_t* problem, const void* x_bf16, const void* router_weight,
+                               float* logits, int32_t* device_status, void* stream);
+
+/* Matrix product in 8-bit integers.  Strides are in elements from one row to
+ * the next, 0 meaning the row's length; x_stride and w_stride are multiples
+ * of 16 (pad rows whose length is not one: what lies between the rows is not
+ * read into the sums). */
+typedef struct {
+  int64_t num_tokens;      /* M >= 0 */
+  int64_t x_stride;        /* >= in_features */
+  int64_t w_stride;        /* >= in_features */
+  int64_t out_stride;      /* >= out_features */
+  int32_t in_features;     /* K, 1 .. 131071 (the 32-bit sum cannot overflow) */
+  int32_t out_features;    /* N >= 1 */
+  int32_t out_fp32;        /* 0: out is BF16, 1: FP32 */
+} moe_int8_matmul_t;
+
+/* out[m, n] = (sum_k x[m,k] * w[n,k]) * x_scale[m] * w_scale[n] + bias[n]:
+ * x int8 [M, K] with one scale per token, w int8 [N, K] with one per channel
+ * (both 16-byte aligned), scales and bias fp32 (bias may be NULL).  The sum
+ * is exact; it is rounded to FP32, multiplied by x_scale, then by w_scale,
+ * and the bias is added, each in FP32; BF16 output rounds once more.
+ * device_status as in moe_router_logits.  out overlaps no input
+ * (MOE_ERR_INVALID_ARG). */
+moe_status_t moe_matmul_int8(const moe_int8_matmul_t* problem, const int8_t* x, const float* x_scale,
+                             const int8_t* w, const float* w_scale, const float* bias, void* out,
+                             int32_t* device_status, void* stream);
+
 /* Where moe_fused leaves its working data inside the workspace, for
  * inspection and testing: byte offsets from the workspace base for a call
  * with this problem (the offsets depend on num_tokens, so pass the call's

@@ -41,6 +41,7 @@ EXPORTS = (
     "moe_fused", "moe_read_status", "moe_status_string", "moe_timing_enable", "moe_timing_read",
     "moe_permute_noalloc", "moe_get_tile_regime", "moe_get_workspace_offsets",
     "moe_workspace_test_hooks", "moe_quantize_nvfp4_rowwise",
+    "moe_rmsnorm_quantize", "moe_router_logits", "moe_matmul_int8",
 )
 
 SLOTS = ("route", "permute", "gather", "gemm1", "zero", "gemm2", "finalize", "combine", "fused")
@@ -89,6 +90,32 @@ class Layout(ctypes.Structure):
         "expert_ids", "num_active", "a_scale_offsets", "tile_offsets")]
 
 
+class NormProblem(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64),
+        ("residual_in_stride", ctypes.c_int64),
+        ("residual_out_stride", ctypes.c_int64),
+        ("hidden", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("residual_fp32", ctypes.c_int32),
+        ("weight_fp32", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class Int8Problem(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64),
+        ("w_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("out_fp32", ctypes.c_int32),
+    ]
+
+
 WS_OFFSET_FIELDS = ("status", "topk_idx", "topk_weights", "expert_counts", "expert_start_indices",
                     "src_info", "slot_to_row", "expert_ids", "num_active", "a_scale_offsets",
                     "tile_offsets", "intermediate", "intermediate_scales", "scale_rows", "accumulator")
@@ -117,6 +144,9 @@ def lib():
             "moe_workspace_init": [vp, sz, vp],
             "moe_workspace_test_hooks": [vp, sz, i32, i32, vp],
             "moe_quantize_nvfp4_rowwise": [P, vp, vp, vp, vp, vp],
+            "moe_rmsnorm_quantize": [ctypes.POINTER(NormProblem)] + [vp] * 9,
+            "moe_router_logits": [P, vp, vp, vp, vp, vp],
+            "moe_matmul_int8": [ctypes.POINTER(Int8Problem)] + [vp] * 8,
             "moe_prepare_weights": [P, ctypes.POINTER(Weights), vp, vp, vp],
             "moe_get_prepared_weights_size": [P, ctypes.POINTER(sz), ctypes.POINTER(sz)],
             "moe_route": [P, vp, vp, vp, vp, vp],
@@ -174,6 +204,7 @@ def _check(fn, code):
 
 TILE_REGIMES = {"auto": 0, "large_m": 1, "small_m": 2}
 ACTIVATIONS = {"swiglu": 0, "swigluoai": 1}
+NORM_FORMATS = {"bf16": 0, "fp8": 1, "mxfp8": 3, "fp8_tensor": 4, "int8": 5}
 
 
 def problem(num_tokens, hidden, intermediate_hidden, num_experts, num_topk,
@@ -198,6 +229,21 @@ def problem_from_dict(d, num_tokens=None, fast_math=1):
                    d["intermediate_hidden"], d["num_experts"], d["num_topk"],
                    d.get("activation_clamp", 10.0), d["format"], fast_math, d.get("tile_regime", "auto"),
                    d.get("shared_expert", 0), d.get("activation", "swiglu"), d.get("activation_alpha", 1.702))
+
+
+def norm_problem(num_tokens, hidden, format="bf16", eps=1e-6, residual_fp32=False, weight_fp32=False, x_stride=0,
+                 residual_in_stride=0, residual_out_stride=0):
+    """A moe_norm_t.  format: a NORM_FORMATS name or code; strides in
+    elements, 0 meaning hidden."""
+    fmt = NORM_FORMATS[format] if isinstance(format, str) else int(format)
+    return NormProblem(int(num_tokens), int(x_stride), int(residual_in_stride), int(residual_out_stride),
+                       int(hidden), fmt, int(residual_fp32), int(weight_fp32), float(eps))
+
+
+def int8_problem(num_tokens, in_features, out_features, out_fp32=False, x_stride=0, w_stride=0, out_stride=0):
+    """A moe_int8_matmul_t; strides in elements, 0 meaning the row's length."""
+    return Int8Problem(int(num_tokens), int(x_stride), int(w_stride), int(out_stride), int(in_features),
+                       int(out_features), int(out_fp32))
 
 
 def act(x, x_scale=None, x_rowwise_scale=None):
@@ -281,6 +327,30 @@ def quantize_nvfp4_rowwise(prob, x_bf16, codes, block_scales, rowwise_scales, st
     """Per-token dynamic NVFP4 quantisation of BF16 activations (see include/moe.h)."""
     _check("moe_quantize_nvfp4_rowwise", lib().moe_quantize_nvfp4_rowwise(
         ctypes.byref(prob), _ptr(x_bf16), _ptr(codes), _ptr(block_scales), _ptr(rowwise_scales), _stream(stream)))
+
+
+def rmsnorm_quantize(prob, x, weight, residual_in=None, residual_out=None, norm_out=None, codes=None, scales=None,
+                     static_scale=None, stream=None):
+    """Residual addition, RMS norm and activation encoding in one pass (see
+    include/moe.h); prob: a NormProblem."""
+    _check("moe_rmsnorm_quantize", lib().moe_rmsnorm_quantize(
+        ctypes.byref(prob), _ptr(x), _ptr(residual_in), _ptr(weight), _ptr(static_scale), _ptr(residual_out),
+        _ptr(norm_out), _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def router_logits(prob, x_bf16, router_weight, logits, device_status, stream=None):
+    """Router logits fp32 [M, E] of BF16 rows (see include/moe.h); prob: the
+    layer's Problem, device_status: an int32 on the device (or a workspace)."""
+    _check("moe_router_logits", lib().moe_router_logits(
+        ctypes.byref(prob), _ptr(x_bf16), _ptr(router_weight), _ptr(logits), _ptr(device_status), _stream(stream)))
+
+
+def matmul_int8(prob, x, x_scale, w, w_scale, out, device_status, bias=None, stream=None):
+    """Product of 8-bit integers with a scale per token and per channel (see
+    include/moe.h); prob: an Int8Problem."""
+    _check("moe_matmul_int8", lib().moe_matmul_int8(
+        ctypes.byref(prob), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(out),
+        _ptr(device_status), _stream(stream)))
 
 
 def permute(prob, topk_idx, lay, ws, ws_bytes, stream=None):

@@ -1,0 +1,200 @@
+"""moe_matmul_int8 and moe_router_logits against the oracle.
+
+The integer product is compared bit for bit: the sum is exact and the
+epilogue's FP32 steps are fixed.  The router's logits: products of two BF16
+numbers are exact in FP32; an instruction adds 16 of them to the sum, each
+such step and the joins of at most 8 partial sums erring by at most one FP32
+step (2^-23) of the largest partial sum, itself at most sum |x w|, and the 16
+products are aligned to the largest of them with as much lost each:
+(H / 16 + 8 + 16) * 2^-23 * sum |x w|.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_routed_03_b200 import api, layer
+from oracle import block as B
+from oracle import formats as F
+from tests.gpu_support import bf16_to_np
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _status():
+    return torch.zeros((1,), dtype=torch.int32, device=DEV)
+
+
+def _codes(shape, g):
+    return torch.randint(-128, 128, shape, generator=g, dtype=torch.int32).to(torch.int8)
+
+
+def _case(M, N, K, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    return (_codes((M, K), g), torch.rand((M,), generator=g) + 0.01, _codes((N, K), g),
+            (torch.rand((N,), generator=g) + 0.01) * 1e-3, torch.randn((N,), generator=g))
+
+
+def _padded(t, stride):
+    """The rows of t, `stride` elements apart, with codes that must not be read between them."""
+    buf = torch.full((t.shape[0], stride), 77, dtype=t.dtype)
+    buf[:, :t.shape[1]] = t
+    return buf.to(DEV)
+
+
+def _check(got, case, bias):
+    x, xs, w, ws, b = case
+    want = B.int8_product(x.numpy(), xs.numpy(), w.numpy(), ws.numpy(), b.numpy() if bias else None)
+    if got.dtype == torch.float32:
+        assert np.array_equal(got.cpu().numpy(), want)
+    else:
+        assert np.array_equal(bf16_to_np(got), F.bf16_decode(F.bf16_encode(want)))
+
+
+SHAPES = [(1, 1, 1), (1, 32, 128), (1, 1001, 4096), (2, 33, 100), (7, 31, 16), (8, 257, 1040), (9, 64, 144),
+          (31, 255, 2048), (33, 96, 384), (64, 1536, 2048), (127, 130, 512), (128, 128, 128), (129, 300, 257),
+          (200, 1, 640), (300, 1001, 1040), (513, 768, 2048), (1, 4096, 7168), (3000, 520, 256), (2500, 2500, 144)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_int8_product_bit_for_bit(M, N, K):
+    case = _case(M, N, K, seed=M + N + K)
+    stride = -(-K // 16) * 16 + 32
+    x, w = _padded(case[0], stride), _padded(case[2], stride)
+    xs, ws, b = case[1].to(DEV), case[3].to(DEV), case[4].to(DEV)
+    status = _status()
+    for fp32, bias in ((True, False), (False, True)):
+        out = torch.empty((M, N), dtype=torch.float32 if fp32 else torch.bfloat16, device=DEV)
+        api.matmul_int8(api.int8_problem(M, K, N, fp32, x_stride=stride, w_stride=stride), x, xs, w, ws, out, status,
+                        bias=b if bias else None)
+        _check(out, case, bias)
+    assert int(status.item()) == api.MOE_OK
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,stride", [(5, 40, 48), (140, 129, 131), (140, 128, 132)])
+def test_int8_output_rows_apart_and_nothing_else_written(out_dtype, M, N, stride):
+    case = _case(M, N, 256, seed=stride)
+    buf = torch.full((M + 2, stride), 5.0, dtype=out_dtype, device=DEV)
+    lin = layer.Int8Linear(case[2].to(DEV), case[3].to(DEV), case[4].to(DEV))
+    out = buf[:M, :N]
+    assert lin.forward(case[0].to(DEV), case[1].to(DEV), out=out) is out
+    _check(out, case, True)
+    assert (buf[M:] == 5).all() and (buf[:M, N:] == 5).all()
+    lin.check_status()
+
+
+def test_int8_largest_sums_do_not_overflow():
+    K = 131071
+    for sign in (-128, 127):
+        x = torch.full((3, K), -128, dtype=torch.int8)
+        w = torch.full((5, K), sign, dtype=torch.int8)
+        case = (x, torch.ones(3), w, torch.ones(5), None)
+        lin = layer.Int8Linear(w.to(DEV), torch.ones(5, device=DEV))
+        xp = _padded(x, 131072)[:, :K]
+        _check(lin.forward(xp, torch.ones(3, device=DEV), out_dtype=torch.float32), case, False)
+
+
+def test_int8_long_reduction_sums_past_24_bits():
+    """Sums whose low bits FP32 does not hold: exact up to the one rounding."""
+    case = _case(4, 48, 8192, seed=2)
+    x, w = case[0].abs().clamp(max=127), case[2].abs().clamp(max=127)
+    case = (x, case[1], w, case[3], case[4])
+    assert B.int8_sums(x.numpy(), w.numpy()).min() > 2 ** 24
+    lin = layer.Int8Linear(w.to(DEV), case[3].to(DEV), case[4].to(DEV))
+    _check(lin.forward(x.to(DEV), case[1].to(DEV), out_dtype=torch.float32), case, True)
+
+
+def test_int8_single_row_of_odd_length():
+    case = _case(1, 20, 77, seed=3)
+    lin = layer.Int8Linear(case[2].to(DEV), case[3].to(DEV), case[4].to(DEV))
+    _check(lin.forward(case[0].to(DEV), case[1].to(DEV)), case, True)
+
+
+def test_int8_scales_that_are_not_finite_follow_the_arithmetic():
+    case = _case(6, 40, 64, seed=4)
+    xs = case[1].clone()
+    xs[2], xs[3], xs[4] = float("nan"), 0.0, float("inf")
+    lin = layer.Int8Linear(case[2].to(DEV), case[3].to(DEV), case[4].to(DEV))
+    out = lin.forward(case[0].to(DEV), xs.to(DEV), out_dtype=torch.float32).cpu()
+    assert torch.isnan(out[2]).all() and torch.equal(out[3], case[4])
+    assert not torch.isfinite(out[4]).any()
+    _check(out[[0, 1, 5]], (case[0][[0, 1, 5]], xs[[0, 1, 5]], case[2], case[3], case[4]), True)
+
+
+def test_int8_two_streams_graphs_and_one_object():
+    """Two captured calls of one object replayed side by side: they share the
+    weights and the status word, and nothing else."""
+    case = _case(96, 700, 1024, seed=5)
+    lin = layer.Int8Linear(case[2].to(DEV), case[3].to(DEV), case[4].to(DEV))
+    cases, graphs, outs, xs = [], [], [], []
+    for s in range(2):
+        c = _case(96, 700, 1024, seed=6 + s)
+        c = (c[0], c[1], case[2], case[3], case[4])
+        x, sc = torch.zeros_like(c[0]).to(DEV), c[1].to(DEV)
+        lin.forward(x, sc)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = lin.forward(x, sc)
+        x.copy_(c[0])
+        cases.append(c), graphs.append(g), outs.append(out), xs.append((x, sc))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for out, c in zip(outs, cases):
+        _check(out, c, True)
+    lin.check_status()
+
+
+# ------------------------------------------------------------------ router
+
+def _router(M, E, H, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((M, H), generator=g).to(torch.bfloat16)
+    w = (torch.randn((E, H), generator=g) * H ** -0.5).to(torch.bfloat16)
+    return x, w
+
+
+def _check_logits(got, x, w):
+    want = B.router_logits(x.double().numpy(), w.double().numpy())
+    size = B.router_logits(x.double().abs().numpy(), w.double().abs().numpy())
+    H = x.shape[1]
+    assert (np.abs(got.double().cpu().numpy() - want) <= (H / 16 + 8 + 16) * 2.0 ** -23 * size).all()
+
+
+@pytest.mark.parametrize("M,E,H", [(1, 1, 256), (1, 256, 7168), (3, 8, 256), (17, 60, 2048), (64, 256, 7168),
+                                   (127, 65, 512), (130, 128, 4096), (777, 60, 2048), (300, 1024, 256),
+                                   (4100, 33, 512), (1500, 1001, 768)])
+def test_router_logits(M, E, H):
+    x, w = _router(M, E, H, seed=M)
+    buf = torch.full((M + 1, E), 3.0, device=DEV)
+    status = _status()
+    api.router_logits(api.problem(M, H, 128, E, 1), x.to(DEV), w.to(DEV), buf, status)
+    _check_logits(buf[:M], x, w)
+    assert (buf[M] == 3).all() and int(status.item()) == api.MOE_OK
+
+
+def test_router_logits_same_bits_every_time():
+    x, w = _router(64, 256, 7168, seed=9)
+    x, w = x.to(DEV), w.to(DEV)
+    status = _status()
+    outs = [torch.empty((64, 256), device=DEV) for _ in range(4)]
+    for o in outs:
+        api.router_logits(api.problem(64, 7168, 128, 256, 1), x, w, o, status)
+    assert all(torch.equal(outs[0], o) for o in outs)
+
+
+def test_router_row_of_nan_stays_alone():
+    x, w = _router(9, 16, 256, seed=10)
+    x[4, 7] = float("nan")
+    out = torch.empty((9, 16), device=DEV)
+    api.router_logits(api.problem(9, 256, 128, 16, 1), x.to(DEV), w.to(DEV), out, _status())
+    assert torch.isnan(out[4]).all()
+    keep = [0, 1, 2, 3, 5, 6, 7, 8]
+    _check_logits(out[keep], x[keep], w)
