@@ -190,8 +190,9 @@ def _ptr(t):
 
 def _stream(s):
     if s is None:
+        # the raw handle alone: a Stream object costs a microsecond a call
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -333,24 +334,28 @@ def rmsnorm_quantize(prob, x, weight, residual_in=None, residual_out=None, norm_
                      static_scale=None, stream=None):
     """Residual addition, RMS norm and activation encoding in one pass (see
     include/moe.h); prob: a NormProblem."""
-    _check("moe_rmsnorm_quantize", lib().moe_rmsnorm_quantize(
-        ctypes.byref(prob), _ptr(x), _ptr(residual_in), _ptr(weight), _ptr(static_scale), _ptr(residual_out),
-        _ptr(norm_out), _ptr(codes), _ptr(scales), _stream(stream)))
+    code = lib().moe_rmsnorm_quantize(prob, _ptr(x), _ptr(residual_in), _ptr(weight), _ptr(static_scale),
+                                      _ptr(residual_out), _ptr(norm_out), _ptr(codes), _ptr(scales), _stream(stream))
+    if code:
+        raise MoEError("moe_rmsnorm_quantize", code)
 
 
 def router_logits(prob, x_bf16, router_weight, logits, device_status, stream=None):
     """Router logits fp32 [M, E] of BF16 rows (see include/moe.h); prob: the
     layer's Problem, device_status: an int32 on the device (or a workspace)."""
-    _check("moe_router_logits", lib().moe_router_logits(
-        ctypes.byref(prob), _ptr(x_bf16), _ptr(router_weight), _ptr(logits), _ptr(device_status), _stream(stream)))
+    code = lib().moe_router_logits(prob, _ptr(x_bf16), _ptr(router_weight), _ptr(logits), _ptr(device_status),
+                                   _stream(stream))
+    if code:
+        raise MoEError("moe_router_logits", code)
 
 
 def matmul_int8(prob, x, x_scale, w, w_scale, out, device_status, bias=None, stream=None):
     """Product of 8-bit integers with a scale per token and per channel (see
     include/moe.h); prob: an Int8Problem."""
-    _check("moe_matmul_int8", lib().moe_matmul_int8(
-        ctypes.byref(prob), _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(out),
-        _ptr(device_status), _stream(stream)))
+    code = lib().moe_matmul_int8(prob, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(out),
+                                 _ptr(device_status), _stream(stream))
+    if code:
+        raise MoEError("moe_matmul_int8", code)
 
 
 def permute(prob, topk_idx, lay, ws, ws_bytes, stream=None):
