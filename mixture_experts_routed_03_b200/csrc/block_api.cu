@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "dense.cuh"
+#include "dense_pair.cuh"
 #include "host.cuh"
 #include "norm.cuh"
 
@@ -95,12 +96,14 @@ struct DensePlan {
 // Tile width and K split by a cost in SM cycles: whole waves of CTAs, each
 // its share of the K blocks at the slower of the loads and the MMAs, plus
 // what a tile costs besides.
+template <int KIND>
 DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
   const int64_t mt = (M + 127) / 128;
   const int a_rows = M >= 128 ? 128 : static_cast<int>((M + 7) / 8 * 8);
-  DensePlan best{256, 1};
+  constexpr int kWidest = KIND == KIND_I8 ? 256 : 128;
+  DensePlan best{kWidest, 1};
   double best_cost = 1e300;
-  for (int nt = 256; nt >= 32; nt /= 2) {
+  for (int nt = kWidest; nt >= 32; nt /= 2) {
     for (int s = 1; s <= 8; s *= 2) {
       if (s > 1 && k_blocks < 4 * s) break;
       const int64_t ctas = mt * ((N + nt - 1) / nt) * s;
@@ -119,12 +122,15 @@ DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
 
 template <int KIND, int NT>
 cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap& tw, cudaStream_t st) {
-  const int stage = (p.a_rows + NT) * 128;
+  // two k blocks a stage while they are small: a wait, a commit and a barrier's
+  // arming for every eight MMAs
+  p.stage_blocks = p.a_rows + NT <= 128 ? 2 : 1;
+  const int stage = (p.a_rows + NT) * 128 * p.stage_blocks;
   // behind the ring: the MMA reads 128 rows of x whatever a_rows is
   const int fixed = 1024 + kDenseHeader + 128 * 128;
   p.stages = (kDenseSmemBytes - fixed) / stage;
   if (p.stages > kDenseMaxStages) p.stages = kDenseMaxStages;
-  const int per_cta = (p.k_blocks + p.splits - 1) / p.splits;
+  const int per_cta = ((p.k_blocks + p.splits - 1) / p.splits + p.stage_blocks - 1) / p.stage_blocks;
   if (p.stages > per_cta) p.stages = per_cta;
   int ring = p.stages * stage + 128 * 128;
   const int rows32 = p.a_rows >= 128 ? 128 : (p.a_rows + 31) / 32 * 32;
@@ -152,13 +158,71 @@ cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap&
   return cudaLaunchKernelEx(&cfg, dense_kernel<KIND, NT>, p, tx, tw);
 }
 
+template <int NT>
+cudaError_t launch_pair(const PairArgs& a, const CUtensorMap& tx, const CUtensorMap& tw, int sms, cudaStream_t st) {
+  const int64_t tiles = int64_t(a.m_tiles) * a.n_tiles;
+  const int pairs = tiles < sms / 2 ? static_cast<int>(tiles) : sms / 2;
+  return launch_k(dense_pair_kernel<NT>, 2 * pairs, kDenseThreads, PairCfg<NT>::kSmemBytes, st, a, tx, tw);
+}
+
+// Tile width of the CTA-pair kernel: the fewest cycles of MMA in the longest
+// pair's tiles.
+int pair_width(int64_t M, int N, int sms) {
+  const int64_t mt = (M + 255) / 256;
+  int best = 256;
+  int64_t best_cost = INT64_MAX;
+  for (int nt = 256; nt >= 128; nt -= 64) {
+    const int64_t tiles = mt * ((N + nt - 1) / nt);
+    const int64_t cost = (tiles + sms / 2 - 1) / (sms / 2) * nt;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = nt;
+    }
+  }
+  return best;
+}
+
+moe_status_t run_pair(const DenseArgs& p, const void* x, const void* w, int64_t k_bytes, int64_t x_stride,
+                      int64_t w_stride, int sms, cudaStream_t st) {
+  PairArgs a{};
+  a.M = p.M;
+  a.N = p.N;
+  a.k_blocks = static_cast<int>((k_bytes + 127) / 128);
+  a.out_fp32 = p.out_fp32;
+  a.x_scale = p.x_scale;
+  a.w_scale = p.w_scale;
+  a.bias = p.bias;
+  a.out = p.out;
+  a.out_stride = p.out_stride;
+  const int per16 = p.out_fp32 ? 4 : 8;
+  a.vec = aligned16(p.out) && p.out_stride % per16 == 0;
+  a.status = p.status;
+  const int nt = pair_width(p.M, p.N, sms);
+  a.m_tiles = static_cast<int>((p.M + 255) / 256);
+  a.n_tiles = (p.N + nt - 1) / nt;
+  if (int64_t(a.m_tiles) * a.n_tiles > 0x7FFFFFFF - sms) return MOE_ERR_UNSUPPORTED;
+  CUtensorMap tx, tw;
+  if (!make_dense_map(&tx, x, k_bytes, p.M, x_stride, 128) || !make_dense_map(&tw, w, k_bytes, p.N, w_stride, nt / 2))
+    return MOE_ERR_CUDA;
+  cudaError_t e;
+  switch (nt) {
+    case 128: e = launch_pair<128>(a, tx, tw, sms, st); break;
+    case 192: e = launch_pair<192>(a, tx, tw, sms, st); break;
+    default: e = launch_pair<256>(a, tx, tw, sms, st); break;
+  }
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 // out [M, N] = x [M, K bytes] w [N, K bytes]^T; strides in bytes.
 template <int KIND>
 moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_bytes, int64_t x_stride, int64_t w_stride,
                        cudaStream_t st) {
+  const int sms = sm_count();
+  if (KIND == KIND_I8 && ((p.M + 255) / 256) * ((p.N + 255) / 256) * 2 >= sms / 2)
+    return run_pair(p, x, w, k_bytes, x_stride, w_stride, sms, st);
   p.k_blocks = static_cast<int>((k_bytes + 127) / 128);
   p.a_rows = p.M >= 128 ? 128 : static_cast<int>((p.M + 7) / 8 * 8);
-  const DensePlan pl = plan_dense(p.M, p.N, p.k_blocks, sm_count());
+  const DensePlan pl = plan_dense<KIND>(p.M, p.N, p.k_blocks, sms);
   p.splits = pl.splits;
   CUtensorMap tx, tw;
   if (!make_dense_map(&tx, x, k_bytes, p.M, x_stride, p.a_rows) ||
@@ -169,7 +233,7 @@ moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_byt
     case 32: e = launch_dense<KIND, 32>(p, tx, tw, st); break;
     case 64: e = launch_dense<KIND, 64>(p, tx, tw, st); break;
     case 128: e = launch_dense<KIND, 128>(p, tx, tw, st); break;
-    default: e = launch_dense<KIND, 256>(p, tx, tw, st); break;
+    default: e = launch_dense<KIND, KIND == KIND_I8 ? 256 : 128>(p, tx, tw, st); break;
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -181,7 +245,7 @@ cudaError_t set_dense_attrs() {
   if ((e = cudaFuncSetAttribute(dense_kernel<KIND, 32>, at, kDenseSmemBytes)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(dense_kernel<KIND, 64>, at, kDenseSmemBytes)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(dense_kernel<KIND, 128>, at, kDenseSmemBytes)) != cudaSuccess) return e;
-  return cudaFuncSetAttribute(dense_kernel<KIND, 256>, at, kDenseSmemBytes);
+  return KIND == KIND_I8 ? cudaFuncSetAttribute(dense_kernel<KIND_I8, 256>, at, kDenseSmemBytes) : cudaSuccess;
 }
 
 bool ensure_block_init() {
@@ -197,7 +261,11 @@ bool ensure_block_init() {
 }  // namespace
 
 cudaError_t moe::block_set_attrs() {
-  const cudaError_t e = set_dense_attrs<KIND_I8>();
+  const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(dense_pair_kernel<128>, at, PairCfg<128>::kSmemBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(dense_pair_kernel<192>, at, PairCfg<192>::kSmemBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(dense_pair_kernel<256>, at, PairCfg<256>::kSmemBytes);
+  if (e == cudaSuccess) e = set_dense_attrs<KIND_I8>();
   return e != cudaSuccess ? e : set_dense_attrs<KIND_BF16>();
 }
 

@@ -10,12 +10,21 @@
 // the K axis.  Operands come by TMA, 128 bytes of K a stage (128-byte
 // swizzle, K-major), rows and columns past the ends filled with zeros; x
 // rows only as many as there are (rounded up to the swizzle's 8), since the
-// accumulator rows of what lies behind them are never read.  Warp 0 loads,
-// warp 1 issues the MMAs into TMEM.  Then each CTA puts its partial tile into
-// its own shared memory, the cluster meets, and the CTAs share out the
-// tile's elements: each is summed over the ranks in their order through
-// distributed shared memory (so results do not depend on timing; no
+// accumulator rows of what lies behind them are never read.  Warp 8 loads,
+// warp 9 issues the MMAs into TMEM, warps 0-7 (two per 32-lane TMEM quarter,
+// one per half of the columns) take the sums out.  Then each CTA puts its
+// partial tile into its own shared memory, the cluster meets, and the CTAs
+// share out the tile's elements: each is summed over the ranks in their order
+// through distributed shared memory (so results do not depend on timing; no
 // workspace, no atomics), scaled and stored.
+//
+// Accumulators.  Consecutive MMAs of one k block go to kAcc different ones:
+// an MMA into the accumulator that its predecessor writes waits for it.  Of
+// BF16 the tensor cores truncate as they add to the accumulator, so a sum's
+// error grows with the number of MMAs behind it (4.4e-6 relative after 256);
+// no accumulator gets more than kChain of them: the epilogue warps then add
+// it to FP32 registers, rounding to nearest, while the MMAs fill the other
+// half of a double buffer.
 //
 // What bounds it: with few rows the stream of w from HBM, which S and NT
 // spread over the SMs; with many rows the tensor cores and the operands'
@@ -38,9 +47,11 @@ namespace moe {
 
 enum { KIND_I8 = 0, KIND_BF16 = 1 };
 
-constexpr int kDenseThreads = 128;
+constexpr int kDenseEpiWarps = 8;
+constexpr int kDenseThreads = (kDenseEpiWarps + 2) * 32;
+constexpr int kDenseEpiThreads = kDenseEpiWarps * 32;
 constexpr int kDenseMaxStages = 24;
-constexpr int kDenseHeader = 1024;            // barriers, flags
+constexpr int kDenseHeader = 4096;            // barriers, flags, the tile's scales
 constexpr int kDenseSmemBytes = 220 * 1024;   // at most
 constexpr int kDenseMinSmemBytes = 80 * 1024;
 
@@ -52,6 +63,7 @@ struct DenseArgs {
   int n_tiles;
   int a_rows;              // x rows loaded per stage: min(128, M rounded up to 8)
   int stages;
+  int stage_blocks;        // k blocks per stage, 1 or 2
   int out_fp32;
   int vec;                 // outputs may be stored four at a time
   const float* x_scale;    // [M] (KIND_I8)
@@ -76,8 +88,10 @@ __host__ __device__ constexpr uint32_t dense_idesc(uint32_t m, uint32_t n) {
   return ((KIND == KIND_I8 ? 2u : 1u) << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
+// Every thread of the cluster.  Not the .aligned form, which a warp whose
+// lanes took different paths must not execute.
 __device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -90,38 +104,66 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ uint4 ld_cluster16(uint32_t saddr, uint32_t rank) {
   uint32_t a;
   uint4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  // volatile keeps it behind the cluster's barrier; without a memory clobber
+  // the loads of all ranks are in flight together
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
+               : "r"(a));
   return v;
+}
+
+// Shape of one tile's accumulators in TMEM.
+template <int KIND, int NT>
+struct DenseCfg {
+  // independent accumulators that the MMAs of a k block rotate over
+  static constexpr int kAcc = KIND == KIND_I8 ? (NT <= 64 ? 4 : NT == 128 ? 2 : 1) : (NT <= 32 ? 4 : NT == 64 ? 2 : 1);
+  static constexpr int kBufs = KIND == KIND_I8 ? 1 : 2;      // BF16: emptied in turn
+  static constexpr int kChain = 16;                          // BF16: MMAs per accumulator until it is emptied
+  static constexpr int kChunk = KIND == KIND_I8 ? (1 << 30) : kChain * kAcc / 4;   // k blocks per buffer
+  static constexpr int kCols = NT * kAcc * kBufs;
+  static constexpr int kPitch = NT * 4 + 16;                 // bytes of a staged row: 16 more spread the banks
+  static_assert(kCols == 128 || kCols == 256, "TMEM columns");
+};
+
+struct DenseHeader {
+  uint64_t full[kDenseMaxStages], empty[kDenseMaxStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;                            // after an abort: the MMAs issued are complete
+  uint32_t tmem;
+  alignas(16) volatile int abort_flag[4];    // raised, wait limit (0: the default); read 16 bytes at a time
+  alignas(16) float xs[128], ws[256], bias[256];   // the tile's scales (KIND_I8)
+};
+static_assert(sizeof(DenseHeader) <= kDenseHeader, "header");
+
+// One lane of the converged warp.  The compiler knows the elected branch to be
+// one thread's: its MMAs and copies take their operands straight from uniform
+// registers.  Behind `lane == 0` instead, four MMAs and a commit took 326
+// cycles to issue and two copies 185, against 148 and 58 here -- what bounded
+// every tile narrower than 128 columns.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
 }
 
 template <int KIND>
 __device__ __forceinline__ uint32_t add_partial(uint32_t a, uint32_t b) {
-  return KIND == KIND_I8 ? a + b : __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  return KIND == KIND_I8 ? a + b : __float_as_uint(__fadd_rn(__uint_as_float(a), __uint_as_float(b)));
 }
 
-// One output element from its sum (its bits: int32 or FP32).
+// Columns [c, c + 4) of row m, those below N; w and b: their scales and bias.
 template <int KIND>
-__device__ __forceinline__ float finish(uint32_t bits, float xs, float ws, float b) {
-  if (KIND == KIND_BF16) return __uint_as_float(bits);
-  return __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(bits)), xs), ws), b);
-}
-
-// Columns [c, c + 4) of row m, those below N.
-template <int KIND>
-__device__ __forceinline__ void store_out4(const DenseArgs& p, int64_t m, int c, const uint32_t (&s)[4]) {
-  const float xs = KIND == KIND_I8 ? __ldg(p.x_scale + m) : 0.0f;
+__device__ __forceinline__ void store_out4(const DenseArgs& p, int64_t m, int c, const uint4& s, float xs,
+                                           const float4& w, const float4& b) {
   float v[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int n = c + j;
-    const bool in = n < p.N;
-    const float ws = KIND == KIND_I8 && in ? __ldg(p.w_scale + n) : 0.0f;
-    const float b = KIND == KIND_I8 && in && p.bias ? __ldg(p.bias + n) : 0.0f;
-    v[j] = finish<KIND>(s[j], xs, ws, b);
+  if (KIND == KIND_BF16) {
+    v[0] = __uint_as_float(s.x), v[1] = __uint_as_float(s.y), v[2] = __uint_as_float(s.z), v[3] = __uint_as_float(s.w);
+  } else {
+    v[0] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(s.x)), xs), w.x), b.x);
+    v[1] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(s.y)), xs), w.y), b.y);
+    v[2] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(s.z)), xs), w.z), b.z);
+    v[3] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(s.w)), xs), w.w), b.w);
   }
   const int64_t o = m * p.out_stride + c;
   if (p.vec && c + 4 <= p.N) {
@@ -142,19 +184,65 @@ __device__ __forceinline__ void store_out4(const DenseArgs& p, int64_t m, int c,
   }
 }
 
+// Sums the tile's elements over the S ranks' staged partials, in rank order,
+// and stores this rank's share.  A thread keeps its column group throughout:
+// the step from one element to the next is a multiple of the groups of a row.
+template <int KIND, int NT, int S>
+__device__ __forceinline__ void join_and_store(const DenseArgs& p, const DenseHeader* hdr, const uint8_t* ring,
+                                               uint32_t rank, int rows, int64_t m0, int n0) {
+  constexpr int kGroups = NT / 4;
+  constexpr int kPitch = DenseCfg<KIND, NT>::kPitch;
+  constexpr int kU = S == 1 ? 4 : 2;            // rows in flight per thread
+  constexpr int kRowStep = S * kDenseEpiThreads / kGroups;
+  const int g0 = static_cast<int>(rank) * kDenseEpiThreads + threadIdx.x;
+  const int c = (g0 % kGroups) * 4;
+  if (n0 + c >= p.N) return;
+  float4 w = make_float4(0.f, 0.f, 0.f, 0.f), b = w;
+  if (KIND == KIND_I8) {
+    w = *reinterpret_cast<const float4*>(hdr->ws + c);
+    b = *reinterpret_cast<const float4*>(hdr->bias + c);
+  }
+  const uint32_t base = smem_u32(ring) + c * 4;
+  for (int r0 = g0 / kGroups; r0 < rows; r0 += kU * kRowStep) {
+    uint4 v[kU][S];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int r = r0 + u * kRowStep;
+      if (r >= rows) continue;
+#pragma unroll
+      for (int q = 0; q < S; ++q) {
+        if (S == 1)
+          v[u][q] = *reinterpret_cast<const uint4*>(ring + r * kPitch + c * 4);
+        else
+          v[u][q] = ld_cluster16(base + r * kPitch, q);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int r = r0 + u * kRowStep;
+      if (r >= rows) continue;
+      uint4 s = v[u][0];
+#pragma unroll
+      for (int q = 1; q < S; ++q) {
+        s.x = add_partial<KIND>(s.x, v[u][q].x);
+        s.y = add_partial<KIND>(s.y, v[u][q].y);
+        s.z = add_partial<KIND>(s.z, v[u][q].z);
+        s.w = add_partial<KIND>(s.w, v[u][q].w);
+      }
+      store_out4<KIND>(p, m0 + r, n0 + c, s, KIND == KIND_I8 ? hdr->xs[r] : 0.0f, w, b);
+    }
+  }
+}
+
 template <int KIND, int NT>
-__global__ void __launch_bounds__(kDenseThreads)
+__global__ void __launch_bounds__(kDenseThreads, 2)
     dense_kernel(const __grid_constant__ DenseArgs p, const __grid_constant__ CUtensorMap tx,
                  const __grid_constant__ CUtensorMap tw) {
-  constexpr uint32_t kCols = NT < 32 ? 32 : NT;
-  constexpr int kPitch = NT * 4 + 16;         // bytes of a staged row: its 16 bytes more spread the banks
+  using Cfg = DenseCfg<KIND, NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
-  uint64_t* empty = full + kDenseMaxStages;
-  uint64_t* done = empty + kDenseMaxStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);  // [0] raised, [1] wait limit (default)
+  DenseHeader* hdr = reinterpret_cast<DenseHeader*>(smem);
+  volatile int* abort_flag = hdr->abort_flag;
   uint8_t* ring = smem + kDenseHeader;
 
   const int warp = threadIdx.x >> 5;
@@ -164,153 +252,219 @@ __global__ void __launch_bounds__(kDenseThreads)
   const int tile = blockIdx.x / S;
   const int n0 = (tile % p.n_tiles) * NT;
   const int64_t m0 = static_cast<int64_t>(tile / p.n_tiles) * 128;
+  const int rows = p.M - m0 < 128 ? static_cast<int>(p.M - m0) : 128;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / S);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / S);
   const uint32_t a_bytes = static_cast<uint32_t>(p.a_rows) * 128u;
-  const uint32_t stage_bytes = a_bytes + NT * 128u;
+  const uint32_t block_bytes = a_bytes + NT * 128u;
+  const uint32_t stage_bytes = block_bytes * p.stage_blocks;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&hdr->full[s], 1);
+      mbar_init(&hdr->empty[s], 1);
     }
-    mbar_init(done, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&hdr->acc_full[b], 1);
+      mbar_init(&hdr->acc_empty[b], kDenseEpiWarps);
+    }
+    mbar_init(&hdr->drain, 1);
     abort_flag[0] = 0;
     abort_flag[1] = 0;
     fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
     prefetch_tensormap(&tx);
     prefetch_tensormap(&tw);
   }
   pdl_wait();
-  if (warp == 1) tmem_alloc(tmem_slot, kCols);
+  if (warp == 9) tmem_alloc(&hdr->tmem, Cfg::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_trigger();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = hdr->tmem;
 
-  if (warp == 0 && lane == 0) {
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-    int stage = 0;
-    uint32_t phase = 0;
-    int issued = 0;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, nullptr, 0)) break;
-      uint8_t* sa = ring + stage * stage_bytes;
-      mbar_arrive_expect_tx(&full[stage], stage_bytes);
-      tma_load_2d(sa, &tx, &full[stage], kb * 128, static_cast<int>(m0));
-      tma_load_2d(sa + a_bytes, &tw, &full[stage], kb * 128, n0);
-      ++issued;
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1u;
+  if (warp == 8) {
+    if (elect_one()) {
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      for (int kb = kb0; kb < kb1; kb += p.stage_blocks) {
+        if (!mbar_wait(&hdr->empty[stage], phase ^ 1u, abort_flag, nullptr, 0)) break;
+        uint8_t* sa = ring + stage * stage_bytes;
+        const bool two = p.stage_blocks == 2 && kb + 1 < kb1;
+        mbar_arrive_expect_tx(&hdr->full[stage], two ? 2 * block_bytes : block_bytes);
+        tma_load_2d(sa + a_bytes, &tw, &hdr->full[stage], kb * 128, n0);
+        tma_load_2d(sa, &tx, &hdr->full[stage], kb * 128, static_cast<int>(m0));
+        if (two) {
+          tma_load_2d(sa + block_bytes + a_bytes, &tw, &hdr->full[stage], kb * 128 + 128, n0);
+          tma_load_2d(sa + block_bytes, &tx, &hdr->full[stage], kb * 128 + 128, static_cast<int>(m0));
+        }
+        ++issued;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (*abort_flag) {
+        // the copies in flight land before the shared memory is given up
+        for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
+          const unsigned long long t0 = globaltimer_ns();
+          while (!mbar_test(&hdr->full[i % p.stages], (i / p.stages) & 1))
+            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+        }
       }
     }
-    if (*abort_flag) {
-      // the copies in flight land before the shared memory is given up
-      for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
+  } else if (warp == 9) {
+    if (elect_one()) {
+      constexpr uint32_t idesc = dense_idesc<KIND>(128, NT);
+      const uint64_t ad0 = sdesc_sw128(smem_u32(ring)), bd0 = sdesc_sw128(smem_u32(ring) + a_bytes);
+      int stage = 0;
+      uint32_t phase = 0;
+      int in = 0, buf = 0;                    // k block of the chunk, accumulator buffer
+      uint32_t buf_phase = 1;
+      for (int kb = kb0; kb < kb1; kb += p.stage_blocks) {
+        if (!mbar_wait(&hdr->full[stage], phase, abort_flag, nullptr, 0)) break;
+        tc_fence_after();
+        const int blocks = kb + p.stage_blocks <= kb1 ? p.stage_blocks : 1;
+        bool go = true;
+        for (int b = 0; b < blocks; ++b) {
+          if (Cfg::kBufs > 1 && in == 0) {
+            go = mbar_wait(&hdr->acc_empty[buf], buf_phase, abort_flag, nullptr, 0);
+            if (!go) break;
+            tc_fence_after();
+          }
+          const uint64_t off = (stage * stage_bytes + b * block_bytes) >> 4;
+          const uint32_t d = tmem + buf * Cfg::kAcc * NT;
+#pragma unroll
+          for (int kc = 0; kc < 4; ++kc) {
+            const uint32_t acc = in > 0 || kc >= Cfg::kAcc;
+            if (KIND == KIND_I8)
+              mma_i8(d + (kc % Cfg::kAcc) * NT, ad0 + off + 2 * kc, bd0 + off + 2 * kc, idesc, acc);
+            else
+              mma_f16(d + (kc % Cfg::kAcc) * NT, ad0 + off + 2 * kc, bd0 + off + 2 * kc, idesc, acc);
+          }
+          ++in;
+          if (Cfg::kBufs > 1 && (in == Cfg::kChunk || kb + b == kb1 - 1)) {
+            mma_commit(&hdr->acc_full[buf]);
+            in = 0;
+            buf ^= 1;
+            buf_phase ^= buf == 0;
+          }
+        }
+        if (!go) break;
+        mma_commit(&hdr->empty[stage]);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (Cfg::kBufs == 1) mma_commit(&hdr->acc_full[0]);
+      if (*abort_flag) {
+        mma_commit(&hdr->drain);
         const unsigned long long t0 = globaltimer_ns();
-        while (!mbar_test(&full[i % p.stages], (i / p.stages) & 1))
+        while (!mbar_test(&hdr->drain, 0))
           if (globaltimer_ns() - t0 > kWaitLimitNs) break;
       }
     }
-  } else if (warp == 1 && lane == 0) {
-    constexpr uint32_t idesc = dense_idesc<KIND>(128, NT);
-    int stage = 0;
-    uint32_t phase = 0;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (!mbar_wait(&full[stage], phase, abort_flag, nullptr, 0)) break;
-      tc_fence_after();
-      const uint32_t sa = smem_u32(ring + stage * stage_bytes);
-      const uint64_t ad = sdesc_sw128(sa), bd = sdesc_sw128(sa + a_bytes);
-#pragma unroll
-      for (int kc = 0; kc < 4; ++kc) {
-        const uint32_t acc = kb > kb0 || kc > 0;
-        if (KIND == KIND_I8)
-          mma_i8(tmem, ad + 2 * kc, bd + 2 * kc, idesc, acc);
-        else
-          mma_f16(tmem, ad + 2 * kc, bd + 2 * kc, idesc, acc);
-      }
-      mma_commit(&empty[stage]);
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1u;
+  } else {
+    // epilogue: the tile's scales while the operands stream in, then the sums
+    if (KIND == KIND_I8) {
+      const int t = threadIdx.x;
+      if (t < rows) hdr->xs[t] = __ldg(p.x_scale + m0 + t);
+      if (t < NT && n0 + t < p.N) {
+        hdr->ws[t] = __ldg(p.w_scale + n0 + t);
+        hdr->bias[t] = p.bias ? __ldg(p.bias + n0 + t) : 0.0f;
       }
     }
-    mma_commit(done);
+    constexpr int kHalf = NT / 2;
+    const int quarter = warp & 3, half = warp >> 2;
+    const bool mine = quarter * 32 < rows;
+    const uint32_t t = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kHalf;
+    const int chunks = (kb1 - kb0 + Cfg::kChunk - 1) / Cfg::kChunk;
+    uint8_t* dst = ring + (quarter * 32 + lane) * Cfg::kPitch + half * kHalf * 4;
+    if (Cfg::kBufs == 1) {
+      mbar_wait(&hdr->acc_full[0], 0, abort_flag, nullptr, 0);
+      __syncwarp();                            // tcgen05.ld wants the warp together
+      tc_fence_after();
+      if (mine) {
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 16) {
+          float v[16];
+          uint32_t s[16];
+#pragma unroll
+          for (int a = 0; a < Cfg::kAcc; ++a) {
+            tmem_ld16(t + a * NT + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              s[j] = a == 0 ? __float_as_uint(v[j]) : add_partial<KIND>(s[j], __float_as_uint(v[j]));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(dst + c * 4 + j * 16) = make_uint4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+        }
+      }
+    } else {
+      float sum[kHalf];
+#pragma unroll
+      for (int j = 0; j < kHalf; ++j) sum[j] = 0.0f;
+      for (int ch = 0; ch < chunks; ++ch) {
+        const int buf = ch & 1;
+        const bool here = mbar_wait(&hdr->acc_full[buf], (ch >> 1) & 1, abort_flag, nullptr, 0);
+        if (!__all_sync(0xFFFFFFFFu, here)) break;
+        tc_fence_after();
+        if (mine) {
+          // a K range whose last chunk is shorter than the rotation leaves
+          // no accumulator out: every k block writes all kAcc of them
+#pragma unroll
+          for (int a = 0; a < Cfg::kAcc; ++a) {
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 16) {
+              float v[16];
+              tmem_ld16(t + (buf * Cfg::kAcc + a) * NT + c, v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[c + j] = __fadd_rn(sum[c + j], v[j]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hdr->acc_empty[buf]);
+      }
+      // the ring is free once the last chunk's MMAs are complete: every load landed before them
+      if (mine) {
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 4)
+          *reinterpret_cast<float4*>(dst + c * 4) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+      }
+    }
+    tc_fence_before();
   }
   __syncwarp();
-
-  // all MMAs complete: the ring is free (an aborted CTA waits for the MMAs
-  // it issued all the same)
-  {
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_test(done, 0)) {
-      if (globaltimer_ns() - t0 > 2 * kWaitLimitNs) {
-        *abort_flag = 1;
-        break;
-      }
-    }
-  }
-  tc_fence_after();
-  __syncthreads();
-  const int rows = p.M - m0 < 128 ? static_cast<int>(p.M - m0) : 128;
-  if (warp * 32 < rows) {
-    uint8_t* dst = ring + (warp * 32 + lane) * kPitch;
-    const uint32_t t = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-#pragma unroll
-    for (int c = 0; c < NT; c += 16) {
-      float v[16];
-      tmem_ld16(t + c, v);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<float4*>(dst + c * 4 + j * 16) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    }
-  }
-  tc_fence_before();
   // an abort anywhere in the cluster keeps all of it from storing
-  if (threadIdx.x == 0 && *abort_flag) record_error(p.status, MOE_ERR_TIMEOUT);
   if (S > 1) cluster_sync_all();
   else __syncthreads();
-  bool ok = true;
-  if (S == 1) {
-    ok = *abort_flag == 0;
-  } else {
-    const uint32_t flag16 = smem_u32(tmem_slot) & ~15u;   // the 16 bytes that hold the flag
-    const uint32_t at = (smem_u32(const_cast<int*>(abort_flag)) & 15u) / 4;
-    for (int r = 0; r < S; ++r) {
-      const uint4 v = ld_cluster16(flag16, r);
-      const uint32_t f[4] = {v.x, v.y, v.z, v.w};
-      ok = ok && f[at] == 0;
+  __syncwarp();
+  const bool raised =
+      S == 1 ? *abort_flag != 0 : lane < S && ld_cluster16(smem_u32(const_cast<int*>(abort_flag)), lane).x != 0;
+  const bool ok = !__any_sync(0xFFFFFFFFu, raised);
+  if (!ok && threadIdx.x == 0) record_error(p.status, MOE_ERR_TIMEOUT);
+  if (ok && warp < kDenseEpiWarps) {
+    switch (S) {
+      case 1: join_and_store<KIND, NT, 1>(p, hdr, ring, rank, rows, m0, n0); break;
+      case 2: join_and_store<KIND, NT, 2>(p, hdr, ring, rank, rows, m0, n0); break;
+      case 4: join_and_store<KIND, NT, 4>(p, hdr, ring, rank, rows, m0, n0); break;
+      default: join_and_store<KIND, NT, 8>(p, hdr, ring, rank, rows, m0, n0); break;
     }
   }
-  if (ok) {
-    constexpr int kGroups = NT / 4;            // column groups of a row
-    const int total = rows * kGroups;
-    const uint32_t ring_u = smem_u32(ring);
-    for (int g = static_cast<int>(rank) * kDenseThreads + threadIdx.x; g < total; g += S * kDenseThreads) {
-      const int r = g / kGroups, c = (g % kGroups) * 4;
-      if (n0 + c >= p.N) continue;
-      const uint32_t at = ring_u + r * kPitch + c * 4;
-      uint32_t s[4];
-      {
-        const uint4 v = S > 1 ? ld_cluster16(at, 0) : *reinterpret_cast<const uint4*>(ring + r * kPitch + c * 4);
-        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-      }
-      for (int q = 1; q < S; ++q) {
-        const uint4 v = ld_cluster16(at, q);
-        s[0] = add_partial<KIND>(s[0], v.x);
-        s[1] = add_partial<KIND>(s[1], v.y);
-        s[2] = add_partial<KIND>(s[2], v.z);
-        s[3] = add_partial<KIND>(s[3], v.w);
-      }
-      store_out4<KIND>(p, m0 + r, n0 + c, s);
-    }
-  }
+  __syncwarp();
   if (S > 1) cluster_sync_all();               // no CTA leaves while its shared memory is read
   else __syncthreads();
+  __syncwarp();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kCols);
+  if (warp == 9) tmem_dealloc(tmem, Cfg::kCols);
 }
 
 }  // namespace moe

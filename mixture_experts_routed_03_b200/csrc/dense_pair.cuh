@@ -1,0 +1,332 @@
+// dense_pair.cuh -- the 8-bit integer product of many rows: a persistent
+// kernel of CTA pairs (tcgen05 cta_group::2), 256 x NT output tiles.
+//
+// Of a tile's operands each CTA of the pair loads 128 rows of x and NT / 2
+// rows of w, and the pair's MMA (M = 256) reads both halves: per MMA cycle an
+// SM takes in two thirds of the bytes that a 128 x 256 tile of its own would.
+// The first CTA's stage barriers count both CTAs' copies and its warp 9
+// issues the pair's MMAs; their commits release the stages and hand over the
+// accumulators in both CTAs.  Each CTA's epilogue warps (0-7, two per 32-lane
+// TMEM quarter, one per half of the columns) take their 128 rows out of one
+// of two accumulators, scale, round and store them while the MMAs fill the
+// other.
+//
+// What bounds it: the tensor cores while a tile's K axis is long; the waves
+// of tiles over the 74 pairs when there are few.
+//
+// Tensor memory, dependents and waits as in dense.cuh.
+#pragma once
+
+#include "dense.cuh"
+
+namespace moe {
+
+constexpr int kPairStages = 6;
+constexpr int kPairRaster = 8;         // m tiles that take turns before n moves on
+
+struct PairArgs {
+  int64_t M;
+  int N;
+  int k_blocks;
+  int m_tiles, n_tiles;
+  int out_fp32;
+  const float* x_scale;
+  const float* w_scale;
+  const float* bias;
+  void* out;
+  int64_t out_stride;
+  int vec;                             // rows of out are 16-byte aligned
+  int* status;
+};
+
+struct PairHeader {
+  uint64_t full[kPairStages], empty[kPairStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  alignas(16) volatile int abort_flag[4];
+  alignas(16) float ws[2][256], bias[2][256];
+};
+
+template <int NT>
+struct PairCfg {
+  static constexpr int kABytes = 128 * 128;
+  static constexpr int kStageBytes = kABytes + NT / 2 * 128;
+  static constexpr int kHeader = 5120;
+  static constexpr int kSmemBytes = 1024 + kHeader + kPairStages * kStageBytes;
+  static constexpr int kCols = 512;    // two accumulators of up to 256 columns
+  static_assert(sizeof(PairHeader) <= kHeader, "header");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t mapa_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+
+// A load into this CTA's shared memory that counts on a barrier of the pair
+// (`bar`: its shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrives on `bar` of both CTAs once the MMAs issued so far are complete.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Whether `p` holds for any of the epilogue's threads, which meet here.
+__device__ __forceinline__ bool epilogue_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q, r;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "barrier.red.or.pred r, 1, %2, q;\n\tselp.u32 %0, 1, 0, r;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p)), "n"(kDenseEpiThreads)
+      : "memory");
+  return r != 0;
+}
+
+// Tile t's position: groups of kPairRaster m tiles, m fastest within a group,
+// so that the tiles in flight share rows of both operands in L2.
+__device__ __forceinline__ void pair_tile(const PairArgs& p, int t, int& mt, int& nt) {
+  const int per_group = kPairRaster * p.n_tiles;
+  const int g = t / per_group, in = t % per_group;
+  const int left = p.m_tiles - g * kPairRaster;
+  const int height = left < kPairRaster ? left : kPairRaster;
+  mt = g * kPairRaster + in % height;
+  nt = in / height;
+}
+
+template <int NT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
+    dense_pair_kernel(const __grid_constant__ PairArgs p, const __grid_constant__ CUtensorMap tx,
+                      const __grid_constant__ CUtensorMap tw) {
+  using Cfg = PairCfg<NT>;
+  constexpr int ST = kPairStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  PairHeader* hdr = reinterpret_cast<PairHeader*>(smem);
+  volatile int* abort_flag = hdr->abort_flag;
+  uint8_t* ring = smem + Cfg::kHeader;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles = p.m_tiles * p.n_tiles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&hdr->full[s], 1);
+      mbar_init(&hdr->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&hdr->acc_full[b], 1);
+      mbar_init(&hdr->acc_empty[b], 2 * kDenseEpiWarps);
+    }
+    mbar_init(&hdr->drain, 1);
+    abort_flag[0] = 0;
+    abort_flag[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tensormap(&tx);
+    prefetch_tensormap(&tw);
+  }
+  __syncwarp();
+  pdl_wait();
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&hdr->tmem)),
+                 "r"(Cfg::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cluster_sync_all();                  // both CTAs' barriers exist before either is signalled
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = hdr->tmem;
+
+  if (warp == 8) {
+    if (elect_one()) {
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool go = true;
+      for (int t = pair; t < tiles && go; t += pairs) {
+        int mt, nt;
+        pair_tile(p, t, mt, nt);
+        // a half without any row loads the tile's first instead (its results are not stored)
+        int64_t m = static_cast<int64_t>(mt) * 256 + rank * 128;
+        if (m >= p.M) m = static_cast<int64_t>(mt) * 256;
+        int n = nt * NT + static_cast<int>(rank) * (NT / 2);
+        if (n >= p.N) n = nt * NT;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          go = mbar_wait(&hdr->empty[stage], phase ^ 1u, abort_flag, nullptr, 0);
+          if (!go) break;
+          uint8_t* sa = ring + stage * Cfg::kStageBytes;
+          const uint32_t bar = mapa_rank(smem_u32(&hdr->full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&hdr->full[stage], 2 * Cfg::kStageBytes);
+          tma_load_2d_pair(sa, &tx, bar, kb * 128, static_cast<int>(m));
+          tma_load_2d_pair(sa + Cfg::kABytes, &tw, bar, kb * 128, n);
+          ++issued;
+          if (++stage == ST) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (*abort_flag && rank == 0) {
+        // both CTAs' copies land before the shared memory is given up
+        for (int64_t i = issued > ST ? issued - ST : 0; i < issued; ++i) {
+          const unsigned long long t0 = globaltimer_ns();
+          while (!mbar_test(&hdr->full[i % ST], (i / ST) & 1))
+            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+        }
+      }
+    }
+  } else if (warp == 9) {
+    if (rank == 0 && elect_one()) {
+      constexpr uint32_t idesc = dense_idesc<KIND_I8>(256, NT);
+      const uint64_t ad0 = sdesc_sw128(smem_u32(ring)), bd0 = sdesc_sw128(smem_u32(ring) + Cfg::kABytes);
+      int stage = 0;
+      uint32_t phase = 0;
+      int buf = 0;
+      uint32_t buf_phase = 1;
+      bool go = true;
+      for (int t = pair; t < tiles && go; t += pairs) {
+        go = mbar_wait(&hdr->acc_empty[buf], buf_phase, abort_flag, nullptr, 0);
+        if (!go) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * 256;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          go = mbar_wait(&hdr->full[stage], phase, abort_flag, nullptr, 0);
+          if (!go) break;
+          tc_fence_after();
+          const uint64_t off = static_cast<uint32_t>(stage * Cfg::kStageBytes) >> 4;
+#pragma unroll
+          for (int kc = 0; kc < 4; ++kc)
+            mma_i8_pair(d, ad0 + off + 2 * kc, bd0 + off + 2 * kc, idesc, kb > 0 || kc > 0);
+          mma_commit_pair(&hdr->empty[stage]);
+          if (++stage == ST) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        mma_commit_pair(&hdr->acc_full[buf]);
+        buf ^= 1;
+        buf_phase ^= buf == 0;
+      }
+      if (*abort_flag) {
+        mma_commit_pair(&hdr->drain);
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_test(&hdr->drain, 0))
+          if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+      }
+    }
+  } else {
+    constexpr int kHalf = NT / 2;
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    int it = 0;
+    for (int t = pair; t < tiles; t += pairs, ++it) {
+      const int buf = it & 1;
+      int mt, nt;
+      pair_tile(p, t, mt, nt);
+      const int64_t m = static_cast<int64_t>(mt) * 256 + rank * 128 + quarter * 32 + lane;
+      const int n0 = nt * NT;
+      // the tile's scales: the buffer written here was last read two tiles
+      // ago, and the barrier of one tile ago lies between
+      for (int c = threadIdx.x; c < NT; c += kDenseEpiThreads) {
+        const bool in = n0 + c < p.N;
+        hdr->ws[buf][c] = in ? __ldg(p.w_scale + n0 + c) : 0.0f;
+        hdr->bias[buf][c] = in && p.bias ? __ldg(p.bias + n0 + c) : 0.0f;
+      }
+      const float xs = m < p.M ? __ldg(p.x_scale + m) : 0.0f;
+      asm volatile("barrier.sync 1, %0;" ::"n"(kDenseEpiThreads) : "memory");
+      const bool here = mbar_wait(&hdr->acc_full[buf], (it >> 1) & 1, abort_flag, nullptr, 0);
+      // the epilogue warps decide together whether to go on: the barriers count them all
+      if (epilogue_any(!here || *abort_flag != 0)) break;
+      tc_fence_after();
+      const int c0 = half * kHalf;
+      const int cols = p.N - n0 - c0 < kHalf ? p.N - n0 - c0 : kHalf;   // of this half, maybe < 1
+      const uint32_t src = tmem + lane_addr + buf * 256 + c0;
+#pragma unroll 1
+      for (int c = 0; c < kHalf; c += 32) {
+        float v[32];
+        __syncwarp();
+        tmem_ld32(src + c, v);
+        if (c + 32 >= kHalf) {
+          // the last of this warp's columns: the accumulator may be written again
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(mapa_rank(smem_u32(&hdr->acc_empty[buf]), 0));
+        }
+        if (m >= p.M || c >= cols) continue;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(&hdr->ws[buf][c0 + c + j]);
+          const float4 b = *reinterpret_cast<const float4*>(&hdr->bias[buf][c0 + c + j]);
+          v[j] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(__float_as_int(v[j])), xs), w.x), b.x);
+          v[j + 1] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(__float_as_int(v[j + 1])), xs), w.y), b.y);
+          v[j + 2] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(__float_as_int(v[j + 2])), xs), w.z), b.z);
+          v[j + 3] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(__float_as_int(v[j + 3])), xs), w.w), b.w);
+        }
+        const int64_t o = m * p.out_stride + n0 + c0 + c;
+        if (p.vec && c + 32 <= cols) {
+          if (p.out_fp32) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              dst[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                  pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (c + j >= cols) break;
+            if (p.out_fp32) static_cast<float*>(p.out)[o + j] = v[j];
+            else static_cast<uint16_t*>(p.out)[o + j] = static_cast<uint16_t>(pack_bf16x2(v[j], 0.0f) & 0xFFFFu);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (threadIdx.x == 0 && *abort_flag) record_error(p.status, MOE_ERR_TIMEOUT);
+  tc_fence_before();
+  cluster_sync_all();                  // neither CTA leaves while the other signals it
+  tc_fence_after();
+  __syncwarp();
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Cfg::kCols) : "memory");
+}
+
+}  // namespace moe

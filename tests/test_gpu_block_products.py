@@ -54,7 +54,8 @@ def _check(got, case, bias):
 
 SHAPES = [(1, 1, 1), (1, 32, 128), (1, 1001, 4096), (2, 33, 100), (7, 31, 16), (8, 257, 1040), (9, 64, 144),
           (31, 255, 2048), (33, 96, 384), (64, 1536, 2048), (127, 130, 512), (128, 128, 128), (129, 300, 257),
-          (200, 1, 640), (300, 1001, 1040), (513, 768, 2048), (1, 4096, 7168), (3000, 520, 256), (2500, 2500, 144)]
+          (200, 1, 640), (300, 1001, 1040), (513, 768, 2048), (1, 4096, 7168), (3000, 520, 256), (2500, 2500, 144),
+          (1300, 1600, 272), (5000, 700, 400), (9473, 257, 130), (2400, 2104, 16), (12000, 129, 1040), (1281, 2305, 2048)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
