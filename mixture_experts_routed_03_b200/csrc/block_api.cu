@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "dense.cuh"
+#include "dense_few.cuh"
 #include "dense_pair.cuh"
 #include "host.cuh"
 #include "norm.cuh"
@@ -88,59 +89,127 @@ bool make_dense_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The output of the CTA-pair kernel: boxes of 128 bytes x 32 rows, 128-byte swizzle.
+bool make_out_map(CUtensorMap* m, void* base, bool fp32, uint64_t cols, uint64_t rows, uint64_t stride) {
+  EncodeFn enc = get_encode();
+  if (!enc) return false;
+  const uint64_t elem = fp32 ? 4 : 2;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {stride * elem};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), 32};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct DensePlan {
-  int nt;       // output columns per tile
-  int splits;   // CTAs that share a tile's K axis
+  int pair;         // the CTA-pair kernel, nt columns wide; else dense_kernel:
+  int nt;           // output columns per tile
+  int splits;       // CTAs that share a tile's K axis
+  int tile_rows;    // output rows per tile
+  double cost;      // estimated ns
 };
 
-// Tile width and K split by a cost in SM cycles: whole waves of CTAs, each
-// its share of the K blocks at the slower of the loads and the MMAs, plus
-// what a tile costs besides.
+// CTAs in clusters of s that run at once at one CTA an SM: clusters live
+// within a GPC, whose SMs they need not fill (132 and 120 of 148 for 4 and 8,
+// by cudaOccupancyMaxActiveClusters).
+int cluster_slots(int s, int sms) { return s <= 2 ? sms / s * s : s == 4 ? sms * 132 / 148 : sms * 120 / 148; }
+
+// Shared memory of dense_kernel: the bytes beside its ring, and whether half
+// an SM's holds three stages (then two CTAs share an SM when there are more
+// CTAs than SMs).
+int dense_fixed_bytes(int block) {
+  // behind the ring: the MMA reads 128 rows of x whatever their number is
+  return 1024 + kDenseHeader + (block < 128 * 128 ? 128 * 128 - block : 0);
+}
+int dense_stage_blocks(int a_rows, int nt) {
+  // two k blocks a stage while they are small: a wait, a commit and a barrier's
+  // arming for every eight MMAs
+  return a_rows + nt <= 128 ? 2 : 1;
+}
+
+// Tile and K split of dense_kernel by estimated time: whole waves of CTAs,
+// each its share of the k blocks at the slowest of issue, loads and MMAs,
+// plus what a tile costs besides.  The constants are a fit to 370 timings (27
+// sizes, every width and split); over those sizes its choices are within 3 %
+// of the best at the median and 23 % at worst.
 template <int KIND>
 DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
-  const int64_t mt = (M + 127) / 128;
-  const int a_rows = M >= 128 ? 128 : static_cast<int>((M + 7) / 8 * 8);
   constexpr int kWidest = KIND == KIND_I8 ? 256 : 128;
-  DensePlan best{kWidest, 1};
-  double best_cost = 1e300;
+  DensePlan best{0, kWidest, 1, 128, 1e300};
   for (int nt = kWidest; nt >= 32; nt /= 2) {
+    const int64_t n_tiles = (N + nt - 1) / nt;
     for (int s = 1; s <= 8; s *= 2) {
       if (s > 1 && k_blocks < 4 * s) break;
-      const int64_t ctas = mt * ((N + nt - 1) / nt) * s;
-      const int64_t waves = (ctas + sms - 1) / sms;
-      const double load = (a_rows + nt) * 128.0 / 60.0, mma = 2.0 * nt;
-      const double blocks = (k_blocks + s - 1) / s;
-      const double cost = waves * (blocks * (load > mma ? load : mma) + 3000.0 + (s > 1 ? 1500.0 : 0.0) + 8.0 * nt);
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = {nt, s};
-      }
+      // as many row tiles as the last wave has room for, none higher than 128
+      const int64_t mt0 = (M + 127) / 128;
+      const int blk0 = (M >= 128 ? 128 : static_cast<int>((M + 7) / 8 * 8)) + nt;
+      const int stage0 = blk0 * 128 * dense_stage_blocks(blk0 - nt, nt);
+      int res = 1;
+      if (mt0 * n_tiles * s > sms && kDenseHalfSmemBytes - dense_fixed_bytes(blk0 * 128) >= 3 * stage0) res = 2;
+      const int64_t slots = int64_t(cluster_slots(s, sms)) * res;
+      const int64_t waves = (mt0 * n_tiles * s + slots - 1) / slots;
+      int64_t mt = waves * slots / (n_tiles * s);
+      if (mt < mt0) mt = mt0;
+      int64_t rows = ((M + mt - 1) / mt + 7) / 8 * 8;
+      if (rows > 128) rows = 128;
+      mt = (M + rows - 1) / rows;
+      const int64_t ctas = mt * n_tiles * s;
+      const int64_t per_sm = (ctas + sms - 1) / sms;
+      const double live = per_sm < res ? static_cast<double>(per_sm) : res;
+      const double issue = 195.0 / dense_stage_blocks(static_cast<int>(rows), nt) + 90.0;
+      const double load = live * (rows + nt) * 128.0 / 127.0;
+      const double mma = live * nt * 1.05;
+      const double block = issue > load ? (issue > mma ? issue : mma) : (load > mma ? load : mma);
+      const int64_t blocks = (k_blocks + s - 1) / s;
+      double cost = 1200.0 + waves * (blocks * block + 1800.0 + 0.14 * rows * nt / s * live +
+                                      (s > 1 ? 1200.0 * std::sqrt(static_cast<double>(s)) : 0.0));
+      const double memory = 3000.0 + static_cast<double>(M + N) * k_blocks * 128.0 / 6000.0;
+      if (cost < memory) cost = memory;
+      if (cost < best.cost) best = {0, nt, s, static_cast<int>(rows), cost};
     }
   }
   return best;
 }
 
+// The CTA-pair kernel's tile width, likewise: waves of tiles, each the slower
+// of its MMAs (or loads) and the epilogue of the tile before it.
+DensePlan plan_pair(int64_t M, int N, int k_blocks, int sms) {
+  DensePlan best{1, 256, 1, 256, 1e300};
+  if (sms < 2) return best;
+  for (int nt = 256; nt >= 128; nt -= 64) {
+    const int64_t tiles = (M + 255) / 256 * ((N + nt - 1) / nt);
+    const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
+    const double mma = 1.06 * nt, load = (128 + nt / 2) * 128.0 / 105.0, epilogue = 12.0 * nt;
+    const double main = k_blocks * (mma > load ? mma : load);
+    const double cost = 3100.0 + waves * (main > epilogue ? main : epilogue) + epilogue;
+    if (cost < best.cost) best = {1, nt, 1, 256, cost};
+  }
+  return best;
+}
+
 template <int KIND, int NT>
-cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap& tw, cudaStream_t st) {
-  // two k blocks a stage while they are small: a wait, a commit and a barrier's
-  // arming for every eight MMAs
-  p.stage_blocks = p.a_rows + NT <= 128 ? 2 : 1;
-  const int stage = (p.a_rows + NT) * 128 * p.stage_blocks;
-  // behind the ring: the MMA reads 128 rows of x whatever a_rows is
-  const int fixed = 1024 + kDenseHeader + 128 * 128;
-  p.stages = (kDenseSmemBytes - fixed) / stage;
+cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap& tw, int sms, cudaStream_t st) {
+  p.stage_blocks = dense_stage_blocks(p.tile_rows, NT);
+  p.n_tiles = (p.N + NT - 1) / NT;
+  const int64_t grid = (p.M + p.tile_rows - 1) / p.tile_rows * p.n_tiles * p.splits;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const int block = (p.tile_rows + NT) * 128, stage = block * p.stage_blocks;
+  const int fixed = dense_fixed_bytes(block);
+  int room = kDenseSmemBytes - fixed;
+  const int half = kDenseHalfSmemBytes - fixed;
+  if (grid > sms && half >= 3 * stage) room = half;
+  p.stages = room / stage;
   if (p.stages > kDenseMaxStages) p.stages = kDenseMaxStages;
   const int per_cta = ((p.k_blocks + p.splits - 1) / p.splits + p.stage_blocks - 1) / p.stage_blocks;
   if (p.stages > per_cta) p.stages = per_cta;
-  int ring = p.stages * stage + 128 * 128;
-  const int rows32 = p.a_rows >= 128 ? 128 : (p.a_rows + 31) / 32 * 32;
+  int ring = p.stages * stage + fixed - 1024 - kDenseHeader;
+  const int rows32 = (p.tile_rows + 31) / 32 * 32;
   const int staging = rows32 * (NT * 4 + 16);
   if (ring < staging) ring = staging;
   int smem = 1024 + kDenseHeader + ring;
   if (smem < kDenseMinSmemBytes) smem = kDenseMinSmemBytes;
-  p.n_tiles = (p.N + NT - 1) / NT;
-  const int64_t grid = (p.M + 127) / 128 * p.n_tiles * p.splits;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kDenseThreads);
@@ -158,31 +227,57 @@ cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap&
   return cudaLaunchKernelEx(&cfg, dense_kernel<KIND, NT>, p, tx, tw);
 }
 
+template <int KIND, int MB, int R, int D>
+cudaError_t launch_few(const FewArgs& a, int sms, cudaStream_t st) {
+  // warps that share a row: as many as it takes to give every SM two blocks,
+  // while each still has a full load of its own
+  int wk = 1;
+  const int rows8 = (a.N + R * kFewWarps - 1) / (R * kFewWarps);
+  while (wk < kFewWarps && rows8 * wk < 2 * sms && a.k_bytes >= 1024 * wk) wk *= 2;
+  const int per_block = kFewWarps / wk * R;
+  const int grid = (a.N + per_block - 1) / per_block;
+  switch (wk) {
+    case 1: return launch_k(dense_few_kernel<KIND, MB, R, D, 1>, grid, kFewWarps * 32, 0, st, a);
+    case 2: return launch_k(dense_few_kernel<KIND, MB, R, D, 2>, grid, kFewWarps * 32, 0, st, a);
+    case 4: return launch_k(dense_few_kernel<KIND, MB, R, D, 4>, grid, kFewWarps * 32, 0, st, a);
+    default: return launch_k(dense_few_kernel<KIND, MB, R, D, 8>, grid, kFewWarps * 32, 0, st, a);
+  }
+}
+
+template <int KIND>
+moe_status_t run_few(const DenseArgs& p, const void* x, const void* w, int64_t k_bytes, int64_t x_stride,
+                     int64_t w_stride, int sms, cudaStream_t st) {
+  FewArgs a{};
+  a.x = static_cast<const uint8_t*>(x);
+  a.w = static_cast<const uint8_t*>(w);
+  a.x_stride = x_stride;
+  a.w_stride = w_stride;
+  a.M = static_cast<int>(p.M);
+  a.N = p.N;
+  a.k_bytes = static_cast<int>(k_bytes);
+  a.out_fp32 = p.out_fp32;
+  a.x_scale = p.x_scale;
+  a.w_scale = p.w_scale;
+  a.bias = p.bias;
+  a.out = p.out;
+  a.out_stride = p.out_stride;
+  cudaError_t e;
+  if (a.M == 1) e = launch_few<KIND, 1, 2, 4>(a, sms, st);
+  else if (a.M == 2 || KIND == KIND_I8) e = launch_few<KIND, 2, 2, 4>(a, sms, st);
+  else if (a.M <= 4) e = launch_few<KIND_BF16, 4, 2, 4>(a, sms, st);
+  else e = launch_few<KIND_BF16, 8, 2, 2>(a, sms, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 template <int NT>
-cudaError_t launch_pair(const PairArgs& a, const CUtensorMap& tx, const CUtensorMap& tw, int sms, cudaStream_t st) {
+cudaError_t launch_pair(const PairArgs& a, const CUtensorMap& tx, const CUtensorMap& tw, const CUtensorMap& tout, int sms,
+                        cudaStream_t st) {
   const int64_t tiles = int64_t(a.m_tiles) * a.n_tiles;
   const int pairs = tiles < sms / 2 ? static_cast<int>(tiles) : sms / 2;
-  return launch_k(dense_pair_kernel<NT>, 2 * pairs, kDenseThreads, PairCfg<NT>::kSmemBytes, st, a, tx, tw);
+  return launch_k(dense_pair_kernel<NT>, 2 * pairs, kDenseThreads, PairCfg<NT>::kSmemBytes, st, a, tx, tw, tout);
 }
 
-// Tile width of the CTA-pair kernel: the fewest cycles of MMA in the longest
-// pair's tiles.
-int pair_width(int64_t M, int N, int sms) {
-  const int64_t mt = (M + 255) / 256;
-  int best = 256;
-  int64_t best_cost = INT64_MAX;
-  for (int nt = 256; nt >= 128; nt -= 64) {
-    const int64_t tiles = mt * ((N + nt - 1) / nt);
-    const int64_t cost = (tiles + sms / 2 - 1) / (sms / 2) * nt;
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = nt;
-    }
-  }
-  return best;
-}
-
-moe_status_t run_pair(const DenseArgs& p, const void* x, const void* w, int64_t k_bytes, int64_t x_stride,
+moe_status_t run_pair(const DenseArgs& p, int nt, const void* x, const void* w, int64_t k_bytes, int64_t x_stride,
                       int64_t w_stride, int sms, cudaStream_t st) {
   PairArgs a{};
   a.M = p.M;
@@ -197,18 +292,18 @@ moe_status_t run_pair(const DenseArgs& p, const void* x, const void* w, int64_t 
   const int per16 = p.out_fp32 ? 4 : 8;
   a.vec = aligned16(p.out) && p.out_stride % per16 == 0;
   a.status = p.status;
-  const int nt = pair_width(p.M, p.N, sms);
   a.m_tiles = static_cast<int>((p.M + 255) / 256);
   a.n_tiles = (p.N + nt - 1) / nt;
   if (int64_t(a.m_tiles) * a.n_tiles > 0x7FFFFFFF - sms) return MOE_ERR_UNSUPPORTED;
-  CUtensorMap tx, tw;
+  CUtensorMap tx, tw, tout{};
   if (!make_dense_map(&tx, x, k_bytes, p.M, x_stride, 128) || !make_dense_map(&tw, w, k_bytes, p.N, w_stride, nt / 2))
     return MOE_ERR_CUDA;
+  if (a.vec && !make_out_map(&tout, p.out, p.out_fp32, p.N, p.M, p.out_stride)) return MOE_ERR_CUDA;
   cudaError_t e;
   switch (nt) {
-    case 128: e = launch_pair<128>(a, tx, tw, sms, st); break;
-    case 192: e = launch_pair<192>(a, tx, tw, sms, st); break;
-    default: e = launch_pair<256>(a, tx, tw, sms, st); break;
+    case 128: e = launch_pair<128>(a, tx, tw, tout, sms, st); break;
+    case 192: e = launch_pair<192>(a, tx, tw, tout, sms, st); break;
+    default: e = launch_pair<256>(a, tx, tw, tout, sms, st); break;
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -218,22 +313,25 @@ template <int KIND>
 moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_bytes, int64_t x_stride, int64_t w_stride,
                        cudaStream_t st) {
   const int sms = sm_count();
-  if (KIND == KIND_I8 && ((p.M + 255) / 256) * ((p.N + 255) / 256) * 2 >= sms / 2)
-    return run_pair(p, x, w, k_bytes, x_stride, w_stride, sms, st);
+  if (p.M <= kFewMaxM<KIND>) return run_few<KIND>(p, x, w, k_bytes, x_stride, w_stride, sms, st);
   p.k_blocks = static_cast<int>((k_bytes + 127) / 128);
-  p.a_rows = p.M >= 128 ? 128 : static_cast<int>((p.M + 7) / 8 * 8);
   const DensePlan pl = plan_dense<KIND>(p.M, p.N, p.k_blocks, sms);
+  if (KIND == KIND_I8) {
+    const DensePlan pp = plan_pair(p.M, p.N, p.k_blocks, sms);
+    if (pp.cost < pl.cost) return run_pair(p, pp.nt, x, w, k_bytes, x_stride, w_stride, sms, st);
+  }
   p.splits = pl.splits;
+  p.tile_rows = pl.tile_rows;
   CUtensorMap tx, tw;
-  if (!make_dense_map(&tx, x, k_bytes, p.M, x_stride, p.a_rows) ||
+  if (!make_dense_map(&tx, x, k_bytes, p.M, x_stride, p.tile_rows) ||
       !make_dense_map(&tw, w, k_bytes, p.N, w_stride, pl.nt))
     return MOE_ERR_CUDA;
   cudaError_t e;
   switch (pl.nt) {
-    case 32: e = launch_dense<KIND, 32>(p, tx, tw, st); break;
-    case 64: e = launch_dense<KIND, 64>(p, tx, tw, st); break;
-    case 128: e = launch_dense<KIND, 128>(p, tx, tw, st); break;
-    default: e = launch_dense<KIND, KIND == KIND_I8 ? 256 : 128>(p, tx, tw, st); break;
+    case 32: e = launch_dense<KIND, 32>(p, tx, tw, sms, st); break;
+    case 64: e = launch_dense<KIND, 64>(p, tx, tw, sms, st); break;
+    case 128: e = launch_dense<KIND, 128>(p, tx, tw, sms, st); break;
+    default: e = launch_dense<KIND, KIND == KIND_I8 ? 256 : 128>(p, tx, tw, sms, st); break;
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

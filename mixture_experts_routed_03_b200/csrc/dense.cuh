@@ -6,11 +6,12 @@
 //   KIND_BF16  BF16 operands, FP32 sum and output: the router's logits
 //              (kind::f16)
 //
-// dense_kernel: one 128 x NT output tile per cluster of S CTAs, which split
-// the K axis.  Operands come by TMA, 128 bytes of K a stage (128-byte
-// swizzle, K-major), rows and columns past the ends filled with zeros; x
-// rows only as many as there are (rounded up to the swizzle's 8), since the
-// accumulator rows of what lies behind them are never read.  Warp 8 loads,
+// dense_kernel: one output tile of up to 128 rows and NT columns per cluster
+// of S CTAs, which split the K axis.  Operands come by TMA, 128 bytes of K a
+// block (128-byte swizzle, K-major), rows and columns past the ends filled
+// with zeros; x rows only as many as the tile has (a multiple of the
+// swizzle's 8), since the accumulator rows of what lies behind them are never
+// read -- so the row tiles are cut to fill the last wave of SMs.  Warp 8 loads,
 // warp 9 issues the MMAs into TMEM, warps 0-7 (two per 32-lane TMEM quarter,
 // one per half of the columns) take the sums out.  Then each CTA puts its
 // partial tile into its own shared memory, the cluster meets, and the CTAs
@@ -33,7 +34,7 @@
 // TMEM is allocated after griddepcontrol.wait and dependents are released
 // after the allocation: a CTA of this kernel never holds tensor memory while
 // it waits for another grid, and a later grid's CTA cannot take what this
-// one still needs.  kMinSmemBytes keeps it at two CTAs an SM, whose
+// one still needs.  kDenseMinSmemBytes keeps it at two CTAs an SM, whose
 // allocations fit together, and off the SMs that the grouped GEMMs hold.
 //
 // Every wait is bounded; a wait that runs out raises the CTA's abort flag,
@@ -53,6 +54,7 @@ constexpr int kDenseEpiThreads = kDenseEpiWarps * 32;
 constexpr int kDenseMaxStages = 24;
 constexpr int kDenseHeader = 4096;            // barriers, flags, the tile's scales
 constexpr int kDenseSmemBytes = 220 * 1024;   // at most
+constexpr int kDenseHalfSmemBytes = 112 * 1024;   // two CTAs an SM
 constexpr int kDenseMinSmemBytes = 80 * 1024;
 
 struct DenseArgs {
@@ -61,7 +63,7 @@ struct DenseArgs {
   int k_blocks;            // ceil(K bytes / 128)
   int splits;              // CTAs per cluster
   int n_tiles;
-  int a_rows;              // x rows loaded per stage: min(128, M rounded up to 8)
+  int tile_rows;           // output rows per tile: a multiple of 8, at most 128
   int stages;
   int stage_blocks;        // k blocks per stage, 1 or 2
   int out_fp32;
@@ -251,11 +253,11 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
   const uint32_t rank = S > 1 ? cluster_rank() : 0;
   const int tile = blockIdx.x / S;
   const int n0 = (tile % p.n_tiles) * NT;
-  const int64_t m0 = static_cast<int64_t>(tile / p.n_tiles) * 128;
-  const int rows = p.M - m0 < 128 ? static_cast<int>(p.M - m0) : 128;
+  const int64_t m0 = static_cast<int64_t>(tile / p.n_tiles) * p.tile_rows;
+  const int rows = p.M - m0 < p.tile_rows ? static_cast<int>(p.M - m0) : p.tile_rows;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / S);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / S);
-  const uint32_t a_bytes = static_cast<uint32_t>(p.a_rows) * 128u;
+  const uint32_t a_bytes = static_cast<uint32_t>(p.tile_rows) * 128u;
   const uint32_t block_bytes = a_bytes + NT * 128u;
   const uint32_t stage_bytes = block_bytes * p.stage_blocks;
 

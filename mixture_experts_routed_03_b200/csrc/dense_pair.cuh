@@ -9,7 +9,10 @@
 // accumulators in both CTAs.  Each CTA's epilogue warps (0-7, two per 32-lane
 // TMEM quarter, one per half of the columns) take their 128 rows out of one
 // of two accumulators, scale, round and store them while the MMAs fill the
-// other.
+// other: 128 bytes of 32 rows at a time, through shared memory and a TMA
+// store (with plain stores of a thread's own row the epilogue of a tile took
+// longer than its MMAs at K = 2048).  Outputs whose rows are not 16-byte
+// aligned are stored element by element.
 //
 // What bounds it: the tensor cores while a tile's K axis is long; the waves
 // of tiles over the 74 pairs when there are few.
@@ -21,7 +24,8 @@
 
 namespace moe {
 
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
+constexpr int kPairOutBytes = 32 * 128;  // a warp's staged outputs: 32 rows x 128 bytes
 constexpr int kPairRaster = 8;         // m tiles that take turns before n moves on
 
 struct PairArgs {
@@ -35,7 +39,7 @@ struct PairArgs {
   const float* bias;
   void* out;
   int64_t out_stride;
-  int vec;                             // rows of out are 16-byte aligned
+  int vec;                             // rows of out are 16-byte aligned: stored by TMA
   int* status;
 };
 
@@ -52,8 +56,8 @@ template <int NT>
 struct PairCfg {
   static constexpr int kABytes = 128 * 128;
   static constexpr int kStageBytes = kABytes + NT / 2 * 128;
-  static constexpr int kHeader = 5120;
-  static constexpr int kSmemBytes = 1024 + kHeader + kPairStages * kStageBytes;
+  static constexpr int kHeader = 5120;     // keeps the ring on a 1024-byte boundary
+  static constexpr int kSmemBytes = 1024 + kHeader + kPairStages * kStageBytes + kDenseEpiWarps * kPairOutBytes;
   static constexpr int kCols = 512;    // two accumulators of up to 256 columns
   static_assert(sizeof(PairHeader) <= kHeader, "header");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -75,6 +79,13 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+}
+
 __device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -94,6 +105,30 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A warp's 32 x 32 outputs, row `lane` of them in v, to rows m0 .. m0 + 31 and
+// columns n .. n + cols - 1 of an output of any alignment: turned around in
+// shared memory, so that the warp stores one row at a time.  (A thread
+// storing its own row touched 32 sectors per instruction: 51 us of 4096 x
+// 1001 x 1040, against 15 here.)
+__device__ __forceinline__ void store_rows(const PairArgs& p, uint8_t* staged, const float (&v)[32], int lane,
+                                           int64_t m0, int n, int cols) {
+  __syncwarp();
+  float* f = reinterpret_cast<float*>(staged);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) f[lane * 32 + (j ^ lane)] = v[j];   // column j at j ^ row: no bank twice
+  __syncwarp();
+  const int rows = p.M - m0 < 32 ? static_cast<int>(p.M - m0) : 32;   // maybe < 1
+  if (lane < cols) {
+    int64_t o = m0 * p.out_stride + n + lane;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r, o += p.out_stride) {
+      const float x = f[r * 32 + (lane ^ r)];
+      if (p.out_fp32) static_cast<float*>(p.out)[o] = x;
+      else static_cast<uint16_t*>(p.out)[o] = static_cast<uint16_t>(pack_bf16x2(x, 0.0f) & 0xFFFFu);
+    }
+  }
 }
 
 // Whether `p` holds for any of the epilogue's threads, which meet here.
@@ -122,7 +157,7 @@ __device__ __forceinline__ void pair_tile(const PairArgs& p, int t, int& mt, int
 template <int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
     dense_pair_kernel(const __grid_constant__ PairArgs p, const __grid_constant__ CUtensorMap tx,
-                      const __grid_constant__ CUtensorMap tw) {
+                      const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tout) {
   using Cfg = PairCfg<NT>;
   constexpr int ST = kPairStages;
   extern __shared__ uint8_t smem_raw[];
@@ -154,6 +189,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
   if (warp == 8 && lane == 0) {
     prefetch_tensormap(&tx);
     prefetch_tensormap(&tw);
+    if (p.vec) prefetch_tensormap(&tout);
   }
   __syncwarp();
   pdl_wait();
@@ -248,9 +284,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
       }
     }
   } else {
-    constexpr int kHalf = NT / 2;
-    const int quarter = warp & 3, half = warp >> 2;
+    // columns of the first and second half, whole 64-column chunks each
+    constexpr int kFirst = (NT / 2 + 63) / 64 * 64;
+    const int quarter = warp & 3, c0 = warp < 4 ? 0 : kFirst;
+    const int width = warp < 4 ? kFirst : NT - kFirst;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    uint8_t* staged = ring + ST * Cfg::kStageBytes + warp * kPairOutBytes;
     int it = 0;
     for (int t = pair; t < tiles; t += pairs, ++it) {
       const int buf = it & 1;
@@ -271,21 +310,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
       // the epilogue warps decide together whether to go on: the barriers count them all
       if (epilogue_any(!here || *abort_flag != 0)) break;
       tc_fence_after();
-      const int c0 = half * kHalf;
-      const int cols = p.N - n0 - c0 < kHalf ? p.N - n0 - c0 : kHalf;   // of this half, maybe < 1
+      const int cols = p.N - n0 - c0 < width ? p.N - n0 - c0 : width;   // of this half, maybe < 1
       const uint32_t src = tmem + lane_addr + buf * 256 + c0;
+      const int chunk = p.out_fp32 ? 32 : 64;           // columns of 128 bytes
 #pragma unroll 1
-      for (int c = 0; c < kHalf; c += 32) {
+      for (int c = 0; c < width; c += 32) {
         float v[32];
         __syncwarp();
         tmem_ld32(src + c, v);
-        if (c + 32 >= kHalf) {
+        if (c + 32 >= width) {
           // the last of this warp's columns: the accumulator may be written again
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(mapa_rank(smem_u32(&hdr->acc_empty[buf]), 0));
         }
-        if (m >= p.M || c >= cols) continue;
+        if (c >= cols) continue;
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
           const float4 w = *reinterpret_cast<const float4*>(&hdr->ws[buf][c0 + c + j]);
@@ -295,29 +334,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
           v[j + 2] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(__float_as_int(v[j + 2])), xs), w.z), b.z);
           v[j + 3] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(__float_as_int(v[j + 3])), xs), w.w), b.w);
         }
-        const int64_t o = m * p.out_stride + n0 + c0 + c;
-        if (p.vec && c + 32 <= cols) {
+        if (p.vec) {
+          // 16-byte piece q of row r sits at q ^ (r mod 8) of its 128 bytes (the store's swizzle)
+          if (c % chunk == 0) {
+            if (lane == 0) bulk_wait_read();            // the chunk before has left the buffer
+            __syncwarp();
+          }
+          uint8_t* dst = staged + lane * 128;
           if (p.out_fp32) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dst[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(dst + ((j ^ (lane & 7)) << 4)) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o);
+            const int q0 = c % chunk / 8;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              dst[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                  pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+              *reinterpret_cast<uint4*>(dst + (((q0 + j) ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                             pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+          }
+          if ((c + 32) % chunk == 0 || c + 32 >= cols || c + 32 >= width) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && m < p.M) {                 // rows and columns past the ends are not stored
+              tma_store_2d(&tout, staged, n0 + c0 + c / chunk * chunk, static_cast<int>(m));
+              bulk_commit();
+            }
           }
         } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (c + j >= cols) break;
-            if (p.out_fp32) static_cast<float*>(p.out)[o + j] = v[j];
-            else static_cast<uint16_t*>(p.out)[o + j] = static_cast<uint16_t>(pack_bf16x2(v[j], 0.0f) & 0xFFFFu);
-          }
+          store_rows(p, staged, v, lane, m - lane, n0 + c0 + c, cols - c < 32 ? cols - c : 32);
         }
       }
     }
+    if (lane == 0) bulk_wait_done();
   }
   __syncwarp();
   if (threadIdx.x == 0 && *abort_flag) record_error(p.status, MOE_ERR_TIMEOUT);
