@@ -427,24 +427,26 @@ typedef struct {
  * with the same stride), weight [H].  Per token, in FP32:
  *   h = x + residual_in,  residual_out = round(h),
  *   y = (h * rstd) * weight,  rstd = 1 / sqrt(sum(h^2) / H + eps)
- * (the unrounded h is normalised), and y, rounded once,
+ * (the unrounded h is normalised; the sum is held in FP64 and the products
+ * carry their rounding errors along, so y is within about one FP32 rounding),
+ * and y, rounded once,
  *   to BF16 in norm_out [M, H] (may be NULL unless the format is BF16), and
  *   to codes [M, H] with scales as the format says:
- *     FP8_E4M3_B128    per 128 columns s = amax / 448, q = e4m3(y * (1/s));
+ *     FP8_E4M3_B128    per 128 columns s = amax / 448, q = e4m3(y / s);
  *                      scales fp32 [M, H/128]
  *     MXFP8            per 32 columns X = floor(log2 amax) - 8 clamped to
  *                      [-127, 127] (-127 where amax = 0), q = e4m3(y * 2^-X);
  *                      scales ue8m0 [M, H/32] = X + 127
- *     FP8_PER_TENSOR   q = e4m3(y * (1/static_scale)); static_scale fp32 [1]
+ *     FP8_PER_TENSOR   q = e4m3(y / static_scale); static_scale fp32 [1]
  *                      on the device, a positive normal number (anything else
  *                      gives NaN codes); scales NULL
- *     INT8_PER_TOKEN   per token s = amax / 127, q = rint(y * (1/s)) in
+ *     INT8_PER_TOKEN   per token s = amax / 127, q = rint(y / s) in
  *                      [-127, 127]; scales fp32 [M]
  *     BF16             codes and scales NULL
  * static_scale is NULL in every other format.  E4M3 saturates at 448.  Where
  * a quotient s is below 2^-126 (a block of zeros), s and its codes are 0.
- * A token whose sum of squares is not finite gives NaN throughout, a block
- * whose amax is not finite NaN in the block: scales NaN (MXFP8: 255), E4M3
+ * A token whose sum of squares leaves FP32's range or is NaN gives NaN
+ * throughout, a block whose amax is not finite NaN in the block: scales NaN (MXFP8: 255), E4M3
  * codes NaN, integer codes 0.  Every pointer is 16-byte aligned, FP32 scales
  * 4-byte; outputs overlap neither inputs nor one another
  * (MOE_ERR_INVALID_ARG). */

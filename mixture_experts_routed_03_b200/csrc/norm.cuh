@@ -11,13 +11,18 @@
 // What bounds it is memory: 2 bytes of x, 2 or 4 of r and of r', 1 of the
 // codes and 2 of the normed row per element, with ~10 operations.  A row
 // stays in registers between the sum of squares, the block maxima and the
-// stores, so each byte crosses once.  One block serves one row, every thread
-// holding NV vectors of 8 consecutive columns, vector v = i * threads + tid,
-// so that 16 (4) neighbouring lanes hold one 128- (32-) column block and its
-// maximum is a few shuffles.
+// stores, so each byte crosses once.  A block serves a row at a time, every
+// thread holding NV vectors of 8 consecutive columns, vector v = i * threads +
+// tid, so that 16 (4) neighbouring lanes hold one 128- (32-) column block and
+// its maximum is a few shuffles.
 //
-// Maxima are taken on the magnitudes' bit patterns as unsigned integers: the
-// order is that of the values, and a NaN, above every number, is kept.
+// Roundings.  A code changes where its value crosses the midpoint of two, so
+// the value is kept to about one FP32 rounding: the warps' FP32 sums of
+// squares (short chains and trees) are added up in FP64, the reciprocal root
+// is refined once in FP64 and split into two FP32 parts, as is its quotient
+// by a block's scale, and the product of the three factors carries its
+// rounding errors along (by FMA) until it is rounded.  Against products
+// rounded one by one a quarter of the codes' flips are left.
 #pragma once
 
 #include "common.cuh"
@@ -40,6 +45,7 @@ struct NormArgs {
   int H;
   int weight_fp32;
   float eps;
+  double inv_H;            // 1 / H
 };
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4& u, float (&v)[8]) {
@@ -66,19 +72,72 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 constexpr uint32_t kInfBits = 0x7F800000u;
 constexpr uint32_t kMinNormalBits = 0x00800000u;
 
-// Scale amax / top and its reciprocal.  A maximum that is not finite gives
+// A number as the sum of two FP32 parts, the second a small part of the
+// first's last place.
+struct Two {
+  float hi, lo;
+};
+
+// 1 / s in two parts (s a positive normal number).
+__device__ __forceinline__ Two reciprocal(float s) {
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  return {inv, __fmul_rn(inv, fmaf(-s, inv, 1.0f))};
+}
+
+// a / kDivisor, correctly rounded where nothing underflows: a quotient from
+// the rounded reciprocal and one correction by the exact remainder
+// (Markstein's method).
+template <int kDivisor>
+__device__ __forceinline__ float divided(float a) {
+  constexpr float d = static_cast<float>(kDivisor), z = 1.0f / d;
+  const float q = __fmul_rn(a, z);
+  return fmaf(fmaf(-d, q, a), z, q);
+}
+
+// Scale amax / kTop and its reciprocal.  A maximum that is not finite gives
 // NaN for both (every code of the block becomes NaN, an 8-bit integer 0); a
 // quotient below the smallest normal FP32 number, whose reciprocal may not
 // exist, gives 0 for both.
-__device__ __forceinline__ float scale_of(uint32_t amax_bits, float top, float& inv) {
+template <int kTop>
+__device__ __forceinline__ float scale_of(uint32_t amax_bits, Two& inv) {
+  const float s = divided<kTop>(__uint_as_float(amax_bits));
+  inv = reciprocal(s);
   if (amax_bits >= kInfBits) {
-    inv = __uint_as_float(0x7FC00000u);
-    return inv;
+    inv = {__uint_as_float(0x7FC00000u), 0.0f};
+    return inv.hi;
   }
-  const float s = __fdiv_rn(__uint_as_float(amax_bits), top);
-  const bool zero = abs_bits(s) < kMinNormalBits;
-  inv = zero ? 0.0f : __frcp_rn(s);
-  return zero ? 0.0f : s;
+  if (abs_bits(s) < kMinNormalBits) {
+    inv = {0.0f, 0.0f};
+    return 0.0f;
+  }
+  return s;
+}
+
+// a * b in two parts.
+__device__ __forceinline__ Two product(const Two& a, const Two& b) {
+  const float hi = __fmul_rn(a.hi, b.hi);
+  return {hi, fmaf(a.lo, b.hi, fmaf(a.hi, b.lo, fmaf(a.hi, b.hi, -hi)))};
+}
+
+// h * w * f, rounded once.
+__device__ __forceinline__ float product3(float h, float w, const Two& f) {
+  const float p = __fmul_rn(h, w);
+  const float e = fmaf(h, w, -p);
+  return fmaf(p, f.hi, fmaf(p, f.lo, __fmul_rn(e, f.hi)));
+}
+
+// The bits of (a maximum of |h w|, as bits) * r; NaN stays NaN.
+__device__ __forceinline__ uint32_t amax_of(uint32_t m, const Two& r) {
+  const float p = __uint_as_float(m);
+  return abs_bits(fmaf(p, r.hi, __fmul_rn(p, r.lo)));
+}
+
+// max(m, |v|); NaN if either is.
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t cvt_s8(float v) {
@@ -87,80 +146,96 @@ __device__ __forceinline__ uint32_t cvt_s8(float v) {
   return static_cast<uint32_t>(r) & 0xFFu;
 }
 
-// 8 values times inv -> 8 E4M3 bytes (round to nearest even, saturating).
-__device__ __forceinline__ uint2 codes_e4m3(const float (&v)[8], float inv) {
+// 8 values -> 8 E4M3 bytes (round to nearest even, saturating).
+__device__ __forceinline__ uint2 codes_e4m3(const float (&v)[8]) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    w[i] = static_cast<uint32_t>(cvt_e4m3x2(__fmul_rn(v[4 * i], inv), __fmul_rn(v[4 * i + 1], inv))) |
-           (static_cast<uint32_t>(cvt_e4m3x2(__fmul_rn(v[4 * i + 2], inv), __fmul_rn(v[4 * i + 3], inv))) << 16);
+    w[i] = static_cast<uint32_t>(cvt_e4m3x2(v[4 * i], v[4 * i + 1])) |
+           (static_cast<uint32_t>(cvt_e4m3x2(v[4 * i + 2], v[4 * i + 3])) << 16);
   return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ uint2 codes_s8(const float (&v)[8], float inv) {
+__device__ __forceinline__ uint2 codes_s8(const float (&v)[8]) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     w[i] = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[i] |= cvt_s8(__fmul_rn(v[4 * i + j], inv)) << (8 * j);
+    for (int j = 0; j < 4; ++j) w[i] |= cvt_s8(v[4 * i + j]) << (8 * j);
   }
   return make_uint2(w[0], w[1]);
 }
 
-// One block per row; blockDim.x a multiple of 32, NV * blockDim.x * 8 >= H.
+__device__ __forceinline__ void load_weight8(const NormArgs& a, int v, float (&w)[8]) {
+  if (a.weight_fp32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + 8 * v);
+    unpack_f32x8(__ldg(p), __ldg(p + 1), w);
+  } else {
+    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + 8 * v)), w);
+  }
+}
+
+struct NormShared {
+  float sum[32];
+  uint32_t top[32];
+};
+
+// One row whose columns h the block's threads hold: vector v = i * blockDim.x
+// + threadIdx.x of 8 columns in h[i] (blockDim.x a multiple of 32).
 template <int FMT, int RES, int NV>
-__global__ void __launch_bounds__(1024) rmsnorm_quantize_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float ssum[32];
-  __shared__ uint32_t smax[32];
-  pdl_trigger();
-  pdl_wait();
-  const int64_t row = blockIdx.x;
+__device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, float (&h)[NV][8], NormShared& sh) {
   const int nvec = a.H / 8;
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int nwarps = blockDim.x >> 5;
 
-  float h[NV][8];
-  float ssq = 0.0f;
+  float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = i * blockDim.x + threadIdx.x;
-    if (v < nvec) {
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(a.x + row * a.x_stride + 8 * v), h[i]);
-      if (RES == NR_BF16) {
-        float r[8];
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.res_in) + row * a.rin_stride + 8 * v),
-                      r);
+    if (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x) >= nvec) continue;
+    float q[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] = __fadd_rn(h[i][j], r[j]);
-      } else if (RES == NR_FP32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.res_in) + row * a.rin_stride + 8 * v);
-        float r[8];
-        unpack_f32x8(p[0], p[1], r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] = __fadd_rn(h[i][j], r[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ssq = fmaf(h[i][j], h[i][j], ssq);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
-    }
+    for (int j = 0; j < 4; ++j) q[j] = fmaf(h[i][j + 4], h[i][j + 4], __fmul_rn(h[i][j], h[i][j]));
+    ss += (q[0] + q[1]) + (q[2] + q[3]);
   }
 #pragma unroll
-  for (int off = 16; off; off >>= 1) ssq += __shfl_xor_sync(0xFFFFFFFFu, ssq, off);
-  if (lane == 0) ssum[warp] = ssq;
+  for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
+  if (lane == 0) sh.sum[warp] = ss;
   __syncthreads();
-  ssq = lane < nwarps ? ssum[lane] : 0.0f;
+  // lanes in groups of 2^k >= nwarps, each group with all the warps' sums
+  const int group = nwarps <= 8 ? 8 : 32;
+  const int from = lane & (group - 1);
+  double ssq = from < nwarps ? static_cast<double>(sh.sum[from]) : 0.0;
+  if (group == 32) {
+    ssq += __shfl_xor_sync(0xFFFFFFFFu, ssq, 16);
+    ssq += __shfl_xor_sync(0xFFFFFFFFu, ssq, 8);
+  }
 #pragma unroll
-  for (int off = 16; off; off >>= 1) ssq += __shfl_xor_sync(0xFFFFFFFFu, ssq, off);
-  // a row whose sum of squares is not finite becomes NaN throughout
-  const float rstd = abs_bits(ssq) >= kInfBits
-                         ? __uint_as_float(0x7FC00000u)
-                         : __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ssq, static_cast<float>(a.H)), a.eps)));
+  for (int off = 4; off; off >>= 1) ssq += __shfl_xor_sync(0xFFFFFFFFu, ssq, off);
+  // rstd = r * 2^e with r in [1, 2): h takes the power of two, which is exact,
+  // so that h * w is of y's size and does not leave FP32's range before y does
+  Two r;
+  float pow2;
+  if (ssq <= 3.4028234663852886e38) {
+    const double mean = fma(ssq, a.inv_H, static_cast<double>(a.eps));
+    const double r0 = static_cast<double>(rsqrtf(static_cast<float>(mean)));
+    const double rstd = r0 * fma(-0.5 * mean * r0, r0, 1.5);
+    const float hi = static_cast<float>(rstd);
+    const uint32_t e = __float_as_uint(hi) & kInfBits;
+    pow2 = __uint_as_float(e);
+    const float back = __uint_as_float((254u << 23) - e);     // 2^-e
+    r.hi = __fmul_rn(hi, back);
+    r.lo = __fmul_rn(static_cast<float>(rstd - static_cast<double>(hi)), back);
+  } else {
+    // a row whose sum of squares leaves FP32 (or is NaN) becomes NaN throughout
+    r = {__uint_as_float(0x7FC00000u), 0.0f};
+    pow2 = 1.0f;
+  }
 
   uint32_t row_max = 0;
+  uint8_t* const codes = a.codes + row * a.H;
+  uint16_t* const normed = a.norm_out + row * a.H;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = i * blockDim.x + threadIdx.x;
@@ -174,32 +249,46 @@ __global__ void __launch_bounds__(1024) rmsnorm_quantize_kernel(const __grid_con
       p[1] = make_float4(h[i][4], h[i][5], h[i][6], h[i][7]);
     }
     float w[8];
-    if (a.weight_fp32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + 8 * v);
-      unpack_f32x8(__ldg(p), __ldg(p + 1), w);
-    } else {
-      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + 8 * v)), w);
-    }
+    load_weight8(a, v, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[i][j] = __fmul_rn(__fmul_rn(h[i][j], rstd), w[j]);
-    if (a.norm_out) *reinterpret_cast<uint4*>(a.norm_out + row * a.H + 8 * v) = pack_bf16x8(h[i]);
+    for (int j = 0; j < 8; ++j) h[i][j] = __fmul_rn(h[i][j], pow2);
+    if (a.norm_out) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(__fmul_rn(h[i][j], w[j]), r.hi);
+      *reinterpret_cast<uint4*>(normed + 8 * v) = pack_bf16x8(y);
+    }
     if (FMT == NQ_FP8T) {
       const uint32_t sb = __float_as_uint(__ldg(a.static_scale));
-      const float inv = sb >= kMinNormalBits && sb < kInfBits ? __frcp_rn(__uint_as_float(sb)) : __uint_as_float(0x7FC00000u);
-      *reinterpret_cast<uint2*>(a.codes + row * a.H + 8 * v) = codes_e4m3(h[i], inv);
+      const bool good = sb >= kMinNormalBits && sb < kInfBits;
+      const Two f = product(r, good ? reciprocal(__uint_as_float(sb)) : Two{__uint_as_float(0x7FC00000u), 0.0f});
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // a product that leaves FP32's range saturates
+        const float big = __fmul_rn(__fmul_rn(h[i][j], w[j]), f.hi);
+        y[j] = abs_bits(big) == kInfBits ? big : product3(h[i][j], w[j], f);
+      }
+      *reinterpret_cast<uint2*>(codes + 8 * v) = codes_e4m3(y);
     }
     if (FMT == NQ_FP8 || FMT == NQ_MXFP8 || FMT == NQ_INT8) {
-      uint32_t m = 0;
+      // the largest |y| is the largest |h w| times r
+      float top = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(h[i][j]));
+      for (int j = 0; j < 8; ++j) top = max_abs(top, __fmul_rn(h[i][j], w[j]));
+      uint32_t m = __float_as_uint(top);       // not negative: ordered as its bits, NaN above all numbers
       if (FMT == NQ_INT8) {
         row_max = max(row_max, m);
       } else if (FMT == NQ_FP8) {
 #pragma unroll
         for (int off = 8; off; off >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-        float inv;
-        const float s = scale_of(m, 448.0f, inv);
-        *reinterpret_cast<uint2*>(a.codes + row * a.H + 8 * v) = codes_e4m3(h[i], inv);
+        Two inv;
+        const float s = scale_of<448>(amax_of(m, r), inv);
+        const Two f = product(r, inv);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = product3(h[i][j], w[j], f);
+        *reinterpret_cast<uint2*>(codes + 8 * v) = codes_e4m3(y);
         if ((lane & 15) == 0) static_cast<float*>(a.scales)[row * (a.H / 128) + v / 16] = s;
       } else {
         // scale 2^X, X = floor(log2 amax) - 8 clamped to [-127, 127], read
@@ -207,12 +296,17 @@ __global__ void __launch_bounds__(1024) rmsnorm_quantize_kernel(const __grid_con
         // NaN scale and NaN codes
 #pragma unroll
         for (int off = 2; off; off >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+        m = amax_of(m, r);
         const int ex = static_cast<int>(m >> 23);
         const int X = max(ex - 127 - 8, -127);
         const bool bad = m >= kInfBits;
-        // 2^-X, X in [-127, 119]: as a normal number for X < 127
+        // 2^-X, X in [-127, 119], a normal number
         const float inv = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 - X) << 23);
-        *reinterpret_cast<uint2*>(a.codes + row * a.H + 8 * v) = codes_e4m3(h[i], inv);
+        const Two f = {__fmul_rn(r.hi, inv), __fmul_rn(r.lo, inv)};
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = product3(h[i][j], w[j], f);
+        *reinterpret_cast<uint2*>(codes + 8 * v) = codes_e4m3(y);
         if ((lane & 3) == 0)
           static_cast<uint8_t*>(a.scales)[row * (a.H / 32) + v / 4] = static_cast<uint8_t>(bad ? 255 : X + 127);
       }
@@ -220,17 +314,108 @@ __global__ void __launch_bounds__(1024) rmsnorm_quantize_kernel(const __grid_con
   }
   if (FMT == NQ_INT8) {
     row_max = __reduce_max_sync(0xFFFFFFFFu, row_max);
-    if (lane == 0) smax[warp] = row_max;
+    if (lane == 0) sh.top[warp] = row_max;
     __syncthreads();
-    row_max = __reduce_max_sync(0xFFFFFFFFu, lane < nwarps ? smax[lane] : 0u);
-    float inv;
-    const float s = scale_of(row_max, 127.0f, inv);
+    row_max = __reduce_max_sync(0xFFFFFFFFu, lane < nwarps ? sh.top[lane] : 0u);
+    Two inv;
+    const float s = scale_of<127>(amax_of(row_max, r), inv);
+    const Two f = product(r, inv);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = i * blockDim.x + threadIdx.x;
-      if (v < nvec) *reinterpret_cast<uint2*>(a.codes + row * a.H + 8 * v) = codes_s8(h[i], inv);
+      if (v >= nvec) continue;
+      float w[8], q[8];
+      load_weight8(a, v, w);                   // again, from L1
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = product3(h[i][j], w[j], f);
+      *reinterpret_cast<uint2*>(codes + 8 * v) = codes_s8(q);
     }
     if (threadIdx.x == 0) static_cast<float*>(a.scales)[row] = s;
+  }
+}
+
+__device__ __forceinline__ void add_bf16x8(const uint4& u, float (&h)[8]) {
+  float r[8];
+  unpack_bf16x8(u, r);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = __fadd_rn(h[j], r[j]);
+}
+
+__device__ __forceinline__ void add_f32x8(const float4& a, const float4& b, float (&h)[8]) {
+  float r[8];
+  unpack_f32x8(a, b, r);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = __fadd_rn(h[j], r[j]);
+}
+
+// One block per row, of at most kThreads threads; registers for kBlocks blocks an SM.
+template <int FMT, int RES, int NV, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) rmsnorm_quantize_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ NormShared sh;
+  pdl_trigger();
+  pdl_wait();
+  const int64_t row = blockIdx.x;
+  const int nvec = a.H / 8;
+  float h[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = i * blockDim.x + threadIdx.x;
+    if (v >= nvec) continue;
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(a.x + row * a.x_stride + 8 * v), h[i]);
+    if (RES == NR_BF16)
+      add_bf16x8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.res_in) + row * a.rin_stride + 8 * v),
+                 h[i]);
+    if (RES == NR_FP32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.res_in) + row * a.rin_stride + 8 * v);
+      add_f32x8(p[0], p[1], h[i]);
+    }
+  }
+  norm_row<FMT, RES, NV>(a, row, h, sh);
+}
+
+// Persistent blocks, one vector a thread, for many short rows, whose blocks
+// would come and go at the rate that they can be launched: each thread copies
+// its own columns of the rows to come into its own slots of shared memory
+// (cp.async, no thread waits for another), kRows rows ahead.
+template <int FMT, int RES, int kRows>
+__global__ void __launch_bounds__(96, 10)
+    rmsnorm_quantize_stream_kernel(const __grid_constant__ NormArgs a, int64_t M) {
+  __shared__ NormShared sh[2];                 // rows take turns: one barrier a row keeps them apart
+  extern __shared__ __align__(16) uint8_t slots[];
+  constexpr int kParts = RES == NR_NONE ? 1 : RES == NR_BF16 ? 2 : 3;   // 16-byte pieces of 8 columns
+  pdl_trigger();
+  pdl_wait();
+  const int T = blockDim.x;                    // = H / 8
+  const int col = 8 * threadIdx.x;
+  uint8_t* mine = slots + threadIdx.x * 16;
+  auto at = [&](int b, int q) { return mine + (b * kParts + q) * T * 16; };   // piece q of slot b
+  auto fetch = [&](int64_t row, int b) {
+    if (row < M) {
+      cp_async16(at(b, 0), a.x + row * a.x_stride + col);
+      if (RES == NR_BF16) cp_async16(at(b, 1), static_cast<const uint16_t*>(a.res_in) + row * a.rin_stride + col);
+      if (RES == NR_FP32) {
+        const float* p = static_cast<const float*>(a.res_in) + row * a.rin_stride + col;
+        cp_async16(at(b, 1), p);
+        cp_async16(at(b, 2), p + 4);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int64_t row = blockIdx.x;
+#pragma unroll
+  for (int b = 0; b < kRows; ++b) fetch(row + b * static_cast<int64_t>(gridDim.x), b);
+  int b = 0, turn = 0;
+  for (; row < M; row += gridDim.x) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRows - 1) : "memory");
+    float h[1][8];
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(at(b, 0)), h[0]);
+    if (RES == NR_BF16) add_bf16x8(*reinterpret_cast<const uint4*>(at(b, 1)), h[0]);
+    if (RES == NR_FP32)
+      add_f32x8(*reinterpret_cast<const float4*>(at(b, 1)), *reinterpret_cast<const float4*>(at(b, 2)), h[0]);
+    fetch(row + kRows * static_cast<int64_t>(gridDim.x), b);
+    norm_row<FMT, RES, 1>(a, row, h, sh[turn]);
+    turn ^= 1;
+    if (++b == kRows) b = 0;
   }
 }
 

@@ -1,15 +1,17 @@
 """moe_rmsnorm_quantize against the float64 oracle.
 
 Tolerances, in units u = 2^-24 (half an FP32 step, relative).  h carries 1
-rounding (3 where the residual sum of two rounded numbers is squared: 2 x 1
-+ 1).  The sum of squares adds at most 32 + 5 + 5 roundings (a thread's chain
-of 4 vectors of 8, two trees of 5) to those 3; the square root halves the
-relative error of its argument: (45 + 2) / 2 < 24, and the division by H, the
-addition of eps, the square root and the reciprocal add under 4.  Two products
-and h itself make y: 24 + 4 + 3 = 31 u < 2^-19, relative, element by element.
-What is rounded to fewer bits must lie between the roundings of y (1 - 2^-19)
-and y (1 + 2^-19) (rounding is monotonic); a code, between those of y / s with
-s the scale that the kernel gave, y's error and two more roundings: 2^-18.
+rounding.  The FP32 sum of a warp's squares: 2 for h, 1 for the product or its
+FMA, 3 for the sum of 8, at most 3 for a thread's 4 vectors, 5 for the lanes;
+FP64 from there, so the mean is within 14 u, and the square root halves that:
+rstd within 7 u.  y, for a scale or BF16: 7 + 1 for h, and at most 3 for
+rstd's first part and two products: 11 u; a scale, the quotient of a maximum:
+12 u.  A code's value: 8 u, its products' errors carried along (terms of order
+u^2), and 1 for the rounding of the result.  All within 16 u = 2^-20, relative,
+element by element.  What is rounded to
+fewer bits must lie between the roundings of v (1 - 2^-20) and v (1 + 2^-20)
+(rounding is monotonic); a code, of y / s with s the scale that the kernel
+gave.
 """
 
 import numpy as np
@@ -22,7 +24,7 @@ from oracle import formats as F
 from tests.gpu_support import bf16_to_np
 
 pytestmark = pytest.mark.gpu
-Y_REL, CODE_REL = 2.0 ** -19, 2.0 ** -18
+Y_REL, CODE_REL = 2.0 ** -20, 2.0 ** -20
 DEV = "cuda:0"
 FORMATS = ["bf16", "fp8", "mxfp8", "fp8_tensor", "int8"]
 
@@ -213,10 +215,23 @@ def test_static_scale_that_is_no_scale_gives_nan_codes(value):
     assert ((out.codes & 0x7F) == 0x7F).all()
 
 
-def test_saturates_at_the_largest_code():
+@pytest.mark.parametrize("value", [1e-6, 2.0 ** -126])
+def test_saturates_at_the_largest_code(value):
     x, _, w, _ = _inputs(4, 256, None, seed=11)
-    out = layer.rmsnorm_quantize(x, w, None, "fp8_tensor", static_scale=torch.tensor([1e-6], device=DEV))
+    out = layer.rmsnorm_quantize(x, w, None, "fp8_tensor", static_scale=torch.tensor([value], device=DEV))
     assert ((out.codes & 0x7F) == 0x7E).all()
+
+
+def test_codes_are_those_of_the_exact_values():
+    """2^20 values: a code differs from the exact value's only at a midpoint,
+    within 2^-21 of it.  Spread evenly over a code's width (2^-3 to 2^-4 of
+    it, both of whose ends count), at most 2 * 16 * 2^-21 of them lie so near:
+    16 expected at most, 48 allowed (8 standard deviations above 16)."""
+    x, r, w, ss = _inputs(256, 4096, "fp32", torch.float32, seed=17)
+    out = layer.rmsnorm_quantize(x, w, r, "fp8_tensor", static_scale=ss)
+    _, y = B.rmsnorm(_f64(x), _f64(r), _f64(w), np.float32(1e-6))
+    want = F.e4m3_encode(y / np.float64(ss.item()))
+    assert (out.codes.cpu().numpy() != want).sum() <= 48
 
 
 def test_mxfp8_exponent_clamp():
