@@ -148,10 +148,15 @@ int dense_fixed_bytes(int block) {
   // behind the ring: the MMA reads 128 rows of x whatever their number is
   return 1024 + kDenseHeader + (block < 128 * 128 ? 128 * 128 - block : 0);
 }
-int dense_stage_blocks(int a_rows, int nt) {
-  // two k blocks a stage while they are small: a wait, a commit and a barrier's
-  // arming for every eight MMAs
-  return a_rows + nt <= 128 ? 2 : 1;
+// k blocks per stage.  Two while they are small: a wait, a commit and a
+// barrier's arming for every eight MMAs.  Two also for BF16 tiles of 128
+// columns that each have an SM and the whole K axis to themselves (8192 x 256
+// x 2048: 14.5 us against 18.5); with a second CTA on the SM, which then does
+// not fit, or a part of K, one is faster (16384 x 128 x 4096, K in two: 30
+// against 36).
+int dense_stage_blocks(int kind, int rows, int nt, int splits, int64_t ctas, int sms) {
+  if (rows + nt <= 128) return 2;
+  return kind == KIND_BF16 && nt == 128 && splits == 1 && ctas <= sms ? 2 : 1;
 }
 
 // Tile and K split of dense_kernel by estimated time: whole waves of CTAs,
@@ -170,7 +175,7 @@ DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
       // as many row tiles as the last wave has room for, none higher than 128
       const int64_t mt0 = (M + 127) / 128;
       const int blk0 = (M >= 128 ? 128 : static_cast<int>((M + 7) / 8 * 8)) + nt;
-      const int stage0 = blk0 * 128 * dense_stage_blocks(blk0 - nt, nt);
+      const int stage0 = blk0 * 128 * dense_stage_blocks(KIND, blk0 - nt, nt, s, mt0 * n_tiles * s, sms);
       int res = 1;
       if (mt0 * n_tiles * s > sms && kDenseHalfSmemBytes - dense_fixed_bytes(blk0 * 128) >= 3 * stage0) res = 2;
       const int64_t slots = int64_t(cluster_slots(s, sms)) * res;
@@ -183,7 +188,7 @@ DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
       const int64_t ctas = mt * n_tiles * s;
       const int64_t per_sm = (ctas + sms - 1) / sms;
       const double live = per_sm < res ? static_cast<double>(per_sm) : res;
-      const double issue = 195.0 / dense_stage_blocks(static_cast<int>(rows), nt) + 90.0;
+      const double issue = 195.0 / dense_stage_blocks(KIND, static_cast<int>(rows), nt, s, ctas, sms) + 90.0;
       const double load = live * (rows + nt) * 128.0 / 127.0;
       const double mma = live * nt * 1.05;
       const double block = issue > load ? (issue > mma ? issue : mma) : (load > mma ? load : mma);
@@ -199,15 +204,15 @@ DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
 }
 
 // The CTA-pair kernel's tile width, likewise: waves of tiles, each the slower
-// of its MMAs (or loads) and the epilogue of the tile before it.
+// of its main loop and the epilogue of the tile before it.
 DensePlan plan_pair(int64_t M, int N, int k_blocks, int sms) {
   DensePlan best{1, 256, 1, 256, 1e300};
   if (sms < 2) return best;
   for (int nt = 256; nt >= 128; nt -= 64) {
     const int64_t tiles = (M + 255) / 256 * ((N + nt - 1) / nt);
     const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
-    const double mma = 1.06 * nt, load = (128 + nt / 2) * 128.0 / 105.0, epilogue = 12.0 * nt;
-    const double main = k_blocks * (mma > load ? mma : load);
+    // 200, 256 and 312 ns a k block were measured for 128, 192 and 256 columns
+    const double main = k_blocks * (88.0 + 0.875 * nt), epilogue = 12.0 * nt;
     const double cost = 3100.0 + waves * (main > epilogue ? main : epilogue) + epilogue;
     if (cost < best.cost) best = {1, nt, 1, 256, cost};
   }
@@ -216,9 +221,9 @@ DensePlan plan_pair(int64_t M, int N, int k_blocks, int sms) {
 
 template <int KIND, int NT>
 cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap& tw, int sms, cudaStream_t st) {
-  p.stage_blocks = dense_stage_blocks(p.tile_rows, NT);
   p.n_tiles = (p.N + NT - 1) / NT;
   const int64_t grid = (p.M + p.tile_rows - 1) / p.tile_rows * p.n_tiles * p.splits;
+  p.stage_blocks = dense_stage_blocks(KIND, p.tile_rows, NT, p.splits, grid, sms);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const int block = (p.tile_rows + NT) * 128, stage = block * p.stage_blocks;
   const int fixed = dense_fixed_bytes(block);

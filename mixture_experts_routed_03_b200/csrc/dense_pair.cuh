@@ -24,7 +24,7 @@
 
 namespace moe {
 
-constexpr int kPairStages = 5;
+constexpr int kPairMaxStages = 8;
 constexpr int kPairOutBytes = 32 * 128;  // a warp's staged outputs: 32 rows x 128 bytes
 constexpr int kPairRaster = 8;         // m tiles that take turns before n moves on
 
@@ -44,7 +44,7 @@ struct PairArgs {
 };
 
 struct PairHeader {
-  uint64_t full[kPairStages], empty[kPairStages];
+  uint64_t full[kPairMaxStages], empty[kPairMaxStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem;
@@ -57,7 +57,10 @@ struct PairCfg {
   static constexpr int kABytes = 128 * 128;
   static constexpr int kStageBytes = kABytes + NT / 2 * 128;
   static constexpr int kHeader = 5120;     // keeps the ring on a 1024-byte boundary
-  static constexpr int kSmemBytes = 1024 + kHeader + kPairStages * kStageBytes + kDenseEpiWarps * kPairOutBytes;
+  static constexpr int kOutBytes = kDenseEpiWarps * kPairOutBytes;
+  static constexpr int kFit = (227 * 1024 - 1024 - kHeader - kOutBytes) / kStageBytes;
+  static constexpr int kStages = kFit < kPairMaxStages ? kFit : kPairMaxStages;   // 5, 6 and 7 of 256, 192 and 128
+  static constexpr int kSmemBytes = 1024 + kHeader + kStages * kStageBytes + kOutBytes;
   static constexpr int kCols = 512;    // two accumulators of up to 256 columns
   static_assert(sizeof(PairHeader) <= kHeader, "header");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -111,7 +114,7 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
 // columns n .. n + cols - 1 of an output of any alignment: turned around in
 // shared memory, so that the warp stores one row at a time.  (A thread
 // storing its own row touched 32 sectors per instruction: 51 us of 4096 x
-// 1001 x 1040, against 15 here.)
+// 1001 x 1040, against 13 here.)
 __device__ __forceinline__ void store_rows(const PairArgs& p, uint8_t* staged, const float (&v)[32], int lane,
                                            int64_t m0, int n, int cols) {
   __syncwarp();
@@ -159,7 +162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
     dense_pair_kernel(const __grid_constant__ PairArgs p, const __grid_constant__ CUtensorMap tx,
                       const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tout) {
   using Cfg = PairCfg<NT>;
-  constexpr int ST = kPairStages;
+  constexpr int ST = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   PairHeader* hdr = reinterpret_cast<PairHeader*>(smem);

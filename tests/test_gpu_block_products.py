@@ -171,7 +171,8 @@ def _check_logits(got, x, w):
 
 @pytest.mark.parametrize("M,E,H", [(1, 1, 256), (1, 256, 7168), (3, 8, 256), (17, 60, 2048), (64, 256, 7168),
                                    (127, 65, 512), (130, 128, 4096), (777, 60, 2048), (300, 1024, 256),
-                                   (4100, 33, 512), (1500, 1001, 768)])
+                                   (4100, 33, 512), (1500, 1001, 768), (9000, 128, 1024), (16384, 60, 512),
+                                   (20001, 300, 768), (3000, 256, 2048), (12345, 64, 4096)])
 def test_router_logits(M, E, H):
     x, w = _router(M, E, H, seed=M)
     buf = torch.full((M + 1, E), 3.0, device=DEV)
