@@ -141,12 +141,20 @@ struct DensePlan {
 // by cudaOccupancyMaxActiveClusters).
 int cluster_slots(int s, int sms) { return s <= 2 ? sms / s * s : s == 4 ? sms * 132 / 148 : sms * 120 / 148; }
 
-// Shared memory of dense_kernel: the bytes beside its ring, and whether half
-// an SM's holds three stages (then two CTAs share an SM when there are more
-// CTAs than SMs).
-int dense_fixed_bytes(int block) {
-  // behind the ring: the MMA reads 128 rows of x whatever their number is
-  return 1024 + kDenseHeader + (block < 128 * 128 ? 128 * 128 - block : 0);
+// Shared memory of dense_kernel: the partial sums that a CTA is sent, whether
+// they are (while they are few bytes; dense.cuh has both ways), and what is needed
+// beside the ring (a `block` is a k block's bytes): the header, the 128 rows
+// of x that an MMA reads whatever their number is, and such partials.
+int dense_staging_bytes(int rows, int nt, int splits) {
+  return (rows + splits - 1) / splits * splits * (nt * 4 + 16);
+}
+bool dense_sent(int rows, int nt, int splits) {
+  return splits > 1 && nt <= 64 && dense_staging_bytes(rows, nt, splits) <= 20 * 1024;
+}
+int dense_behind_bytes(int block) { return block < 128 * 128 ? 128 * 128 - block : 0; }
+int dense_fixed_bytes(int block, int rows, int nt, int splits) {
+  return 1024 + kDenseHeader + dense_behind_bytes(block) +
+         (dense_sent(rows, nt, splits) ? dense_staging_bytes(rows, nt, splits) : 0);
 }
 // k blocks per stage.  Two while they are small: a wait, a commit and a
 // barrier's arming for every eight MMAs.  Two also for BF16 tiles of 128
@@ -177,7 +185,7 @@ DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
       const int blk0 = (M >= 128 ? 128 : static_cast<int>((M + 7) / 8 * 8)) + nt;
       const int stage0 = blk0 * 128 * dense_stage_blocks(KIND, blk0 - nt, nt, s, mt0 * n_tiles * s, sms);
       int res = 1;
-      if (mt0 * n_tiles * s > sms && kDenseHalfSmemBytes - dense_fixed_bytes(blk0 * 128) >= 3 * stage0) res = 2;
+      if (mt0 * n_tiles * s > sms && kDenseHalfSmemBytes - dense_fixed_bytes(blk0 * 128, blk0 - nt, nt, s) >= 3 * stage0) res = 2;
       const int64_t slots = int64_t(cluster_slots(s, sms)) * res;
       const int64_t waves = (mt0 * n_tiles * s + slots - 1) / slots;
       int64_t mt = waves * slots / (n_tiles * s);
@@ -226,7 +234,9 @@ cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap&
   p.stage_blocks = dense_stage_blocks(KIND, p.tile_rows, NT, p.splits, grid, sms);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const int block = (p.tile_rows + NT) * 128, stage = block * p.stage_blocks;
-  const int fixed = dense_fixed_bytes(block);
+  const int fixed = dense_fixed_bytes(block, p.tile_rows, NT, p.splits);
+  // two CTAs an SM where there are more than SMs and a ring of three stages
+  // fits in half of the shared memory
   int room = kDenseSmemBytes - fixed;
   const int half = kDenseHalfSmemBytes - fixed;
   if (grid > sms && half >= 3 * stage) room = half;
@@ -234,11 +244,10 @@ cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap&
   if (p.stages > kDenseMaxStages) p.stages = kDenseMaxStages;
   const int per_cta = ((p.k_blocks + p.splits - 1) / p.splits + p.stage_blocks - 1) / p.stage_blocks;
   if (p.stages > per_cta) p.stages = per_cta;
-  int ring = p.stages * stage + fixed - 1024 - kDenseHeader;
-  const int rows32 = (p.tile_rows + 31) / 32 * 32;
-  const int staging = rows32 * (NT * 4 + 16);
-  if (ring < staging) ring = staging;
-  int smem = 1024 + kDenseHeader + ring;
+  p.ring_bytes = p.stages * stage + dense_behind_bytes(block);
+  const bool sent = dense_sent(p.tile_rows, NT, p.splits);
+  const int staging = dense_staging_bytes(p.tile_rows, NT, p.splits);
+  int smem = 1024 + kDenseHeader + (sent ? p.ring_bytes + staging : p.ring_bytes > staging ? p.ring_bytes : staging);
   if (smem < kDenseMinSmemBytes) smem = kDenseMinSmemBytes;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -254,7 +263,8 @@ cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap&
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, dense_kernel<KIND, NT>, p, tx, tw);
+  if (NT <= 64 && sent) return cudaLaunchKernelEx(&cfg, dense_kernel<KIND, NT <= 64 ? NT : 64, true>, p, tx, tw);
+  return cudaLaunchKernelEx(&cfg, dense_kernel<KIND, NT, false>, p, tx, tw);
 }
 
 template <int KIND, int MB, int R, int D>
@@ -366,14 +376,20 @@ moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_byt
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+template <int KIND, int NT, bool kSent>
+cudaError_t set_dense_attr() {
+  return cudaFuncSetAttribute(dense_kernel<KIND, NT, kSent>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmemBytes);
+}
+
 template <int KIND>
 cudaError_t set_dense_attrs() {
-  const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e;
-  if ((e = cudaFuncSetAttribute(dense_kernel<KIND, 32>, at, kDenseSmemBytes)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(dense_kernel<KIND, 64>, at, kDenseSmemBytes)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(dense_kernel<KIND, 128>, at, kDenseSmemBytes)) != cudaSuccess) return e;
-  return KIND == KIND_I8 ? cudaFuncSetAttribute(dense_kernel<KIND_I8, 256>, at, kDenseSmemBytes) : cudaSuccess;
+  cudaError_t e = set_dense_attr<KIND, 32, true>();
+  if (e == cudaSuccess) e = set_dense_attr<KIND, 64, true>();
+  if (e == cudaSuccess) e = set_dense_attr<KIND, 32, false>();
+  if (e == cudaSuccess) e = set_dense_attr<KIND, 64, false>();
+  if (e == cudaSuccess) e = set_dense_attr<KIND, 128, false>();
+  if (e == cudaSuccess && KIND == KIND_I8) e = set_dense_attr<KIND_I8, 256, false>();
+  return e;
 }
 
 bool ensure_block_init() {

@@ -13,11 +13,16 @@
 // swizzle's 8), since the accumulator rows of what lies behind them are never
 // read -- so the row tiles are cut to fill the last wave of SMs.  Warp 8 loads,
 // warp 9 issues the MMAs into TMEM, warps 0-7 (two per 32-lane TMEM quarter,
-// one per half of the columns) take the sums out.  Then each CTA puts its
-// partial tile into its own shared memory, the cluster meets, and the CTAs
-// share out the tile's elements: each is summed over the ranks in their order
-// through distributed shared memory (so results do not depend on timing; no
-// workspace, no atomics), scaled and stored.
+// one per half of the columns) take the sums out.  The CTAs of a cluster share
+// out the tile's rows (row r belongs to rank r mod S): every owner sums its
+// rows over the ranks in their order (so results do not depend on timing; no
+// workspace, no atomics), scales and stores them.  The partials cross through
+// distributed shared memory, in one of two ways.  Few bytes are written into
+// the owner's memory, beside its ring, and the cluster meets once (64 x 256 x
+// 7168 BF16: 7.3 us against 7.9 the other way).  Otherwise each CTA leaves its
+// partial tile in its own ring, free by then, the cluster meets, owners read
+// the others', and the cluster meets again before any CTA leaves (4096 x 256 x
+// 7168: 24 us against 26).
 //
 // Accumulators.  Consecutive MMAs of one k block go to kAcc different ones:
 // an MMA into the accumulator that its predecessor writes waits for it.  Of
@@ -66,6 +71,7 @@ struct DenseArgs {
   int tile_rows;           // output rows per tile: a multiple of 8, at most 128
   int stages;
   int stage_blocks;        // k blocks per stage, 1 or 2
+  int ring_bytes;
   int out_fp32;
   int vec;                 // outputs may be stored four at a time
   const float* x_scale;    // [M] (KIND_I8)
@@ -90,10 +96,13 @@ __host__ __device__ constexpr uint32_t dense_idesc(uint32_t m, uint32_t n) {
   return ((KIND == KIND_I8 ? 2u : 1u) << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// Every thread of the cluster.  Not the .aligned form, which a warp whose
+// Every thread of the cluster.  Not the .aligned forms, which a warp whose
 // lanes took different paths must not execute.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -102,17 +111,30 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
-// 16 bytes at the local shared address `saddr` of the cluster's CTA `rank`.
-__device__ __forceinline__ uint4 ld_cluster16(uint32_t saddr, uint32_t rank) {
-  uint32_t a;
+// The local shared address `saddr` in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t mapa_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ uint4 ld_cluster16(uint32_t addr) {
   uint4 v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   // volatile keeps it behind the cluster's barrier; without a memory clobber
   // the loads of all ranks are in flight together
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
+               : "r"(addr));
   return v;
+}
+
+__device__ __forceinline__ void st_cluster16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+__device__ __forceinline__ void st_cluster4(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Shape of one tile's accumulators in TMEM.
@@ -133,7 +155,8 @@ struct DenseHeader {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;                            // after an abort: the MMAs issued are complete
   uint32_t tmem;
-  alignas(16) volatile int abort_flag[4];    // raised, wait limit (0: the default); read 16 bytes at a time
+  alignas(16) volatile int abort_flag[4];    // raised, wait limit (0: the default)
+  volatile uint32_t raised[8];               // the ranks' abort flags at the join
   alignas(16) float xs[128], ws[256], bias[256];   // the tile's scales (KIND_I8)
 };
 static_assert(sizeof(DenseHeader) <= kDenseHeader, "header");
@@ -186,43 +209,45 @@ __device__ __forceinline__ void store_out4(const DenseArgs& p, int64_t m, int c,
   }
 }
 
-// Sums the tile's elements over the S ranks' staged partials, in rank order,
-// and stores this rank's share.  A thread keeps its column group throughout:
-// the step from one element to the next is a multiple of the groups of a row.
-template <int KIND, int NT, int S>
-__device__ __forceinline__ void join_and_store(const DenseArgs& p, const DenseHeader* hdr, const uint8_t* ring,
-                                               uint32_t rank, int rows, int64_t m0, int n0) {
+// Sums this rank's rows (rank, rank + S, ...) over the S ranks' partials, in
+// rank order, and stores them.  Rank q's partial of row r is row q * slots + r
+// / S of this CTA's staging if it was sent here, else row r of rank q's.  A thread keeps its column group throughout: the step
+// from one element to the next is a multiple of the groups of a row.
+template <int KIND, int NT, bool kSent, int S>
+__device__ __forceinline__ void join_and_store(const DenseArgs& p, const DenseHeader* hdr, const uint8_t* staged,
+                                               int slots, int rank, int rows, int64_t m0, int n0) {
   constexpr int kGroups = NT / 4;
   constexpr int kPitch = DenseCfg<KIND, NT>::kPitch;
-  constexpr int kU = S == 1 ? 4 : 2;            // rows in flight per thread
-  constexpr int kRowStep = S * kDenseEpiThreads / kGroups;
-  const int g0 = static_cast<int>(rank) * kDenseEpiThreads + threadIdx.x;
-  const int c = (g0 % kGroups) * 4;
+  constexpr int kU = S <= 2 ? 4 : 2;            // rows in flight per thread
+  constexpr int kRowStep = kDenseEpiThreads / kGroups;
+  const int c = (threadIdx.x % kGroups) * 4;
   if (n0 + c >= p.N) return;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f), b = w;
   if (KIND == KIND_I8) {
     w = *reinterpret_cast<const float4*>(hdr->ws + c);
     b = *reinterpret_cast<const float4*>(hdr->bias + c);
   }
-  const uint32_t base = smem_u32(ring) + c * 4;
-  for (int r0 = g0 / kGroups; r0 < rows; r0 += kU * kRowStep) {
+  const int own = (rows - rank + S - 1) / S;    // rows of this rank
+  const uint32_t base = smem_u32(staged) + c * 4;
+  for (int i0 = threadIdx.x / kGroups; i0 < own; i0 += kU * kRowStep) {
     uint4 v[kU][S];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int r = r0 + u * kRowStep;
-      if (r >= rows) continue;
+      const int i = i0 + u * kRowStep;
+      if (i >= own) continue;
 #pragma unroll
       for (int q = 0; q < S; ++q) {
         if (S == 1)
-          v[u][q] = *reinterpret_cast<const uint4*>(ring + r * kPitch + c * 4);
+          v[u][q] = *reinterpret_cast<const uint4*>(staged + i * kPitch + c * 4);
         else
-          v[u][q] = ld_cluster16(base + r * kPitch, q);
+          v[u][q] = ld_cluster16(kSent ? base + (q * slots + i) * kPitch
+                                          : mapa_rank(base + (i * S + rank) * kPitch, q));
       }
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int r = r0 + u * kRowStep;
-      if (r >= rows) continue;
+      const int i = i0 + u * kRowStep;
+      if (i >= own) continue;
       uint4 s = v[u][0];
 #pragma unroll
       for (int q = 1; q < S; ++q) {
@@ -231,12 +256,14 @@ __device__ __forceinline__ void join_and_store(const DenseArgs& p, const DenseHe
         s.z = add_partial<KIND>(s.z, v[u][q].z);
         s.w = add_partial<KIND>(s.w, v[u][q].w);
       }
+      const int r = i * S + rank;
       store_out4<KIND>(p, m0 + r, n0 + c, s, KIND == KIND_I8 ? hdr->xs[r] : 0.0f, w, b);
     }
   }
 }
 
-template <int KIND, int NT>
+// kSent: the partials of a cluster (S > 1) are sent to their owners.
+template <int KIND, int NT, bool kSent>
 __global__ void __launch_bounds__(kDenseThreads, 2)
     dense_kernel(const __grid_constant__ DenseArgs p, const __grid_constant__ CUtensorMap tx,
                  const __grid_constant__ CUtensorMap tw) {
@@ -246,6 +273,8 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
   DenseHeader* hdr = reinterpret_cast<DenseHeader*>(smem);
   volatile int* abort_flag = hdr->abort_flag;
   uint8_t* ring = smem + kDenseHeader;
+  // partials: sent ones beside the ring, which may still be in use when they come
+  uint8_t* staged = ring + (kSent ? p.ring_bytes : 0);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -286,6 +315,9 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = hdr->tmem;
+  // the CTAs of a cluster are there before any of them writes into another
+  if (kSent) cluster_arrive();
+  const int slots = (p.tile_rows + S - 1) / S;
 
   if (warp == 8) {
     if (elect_one()) {
@@ -383,15 +415,19 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
     }
     constexpr int kHalf = NT / 2;
     const int quarter = warp & 3, half = warp >> 2;
-    const bool mine = quarter * 32 < rows;
     const uint32_t t = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kHalf;
     const int chunks = (kb1 - kb0 + Cfg::kChunk - 1) / Cfg::kChunk;
-    uint8_t* dst = ring + (quarter * 32 + lane) * Cfg::kPitch + half * kHalf * 4;
+    const int row = quarter * 32 + lane;
+    const uint32_t at = smem_u32(staged) + (kSent ? rank * slots + row / S : row) * Cfg::kPitch + half * kHalf * 4;
+    const uint32_t dst = kSent ? mapa_rank(at, row % S) : at;
+    if (kSent) cluster_wait();
+    const bool mine = row < p.tile_rows;
+    const bool any = quarter * 32 < rows;
     if (Cfg::kBufs == 1) {
       mbar_wait(&hdr->acc_full[0], 0, abort_flag, nullptr, 0);
       __syncwarp();                            // tcgen05.ld wants the warp together
       tc_fence_after();
-      if (mine) {
+      if (any) {
 #pragma unroll
         for (int c = 0; c < kHalf; c += 16) {
           float v[16];
@@ -405,7 +441,7 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(dst + c * 4 + j * 16) = make_uint4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+            if (mine) st_cluster16(dst + c * 4 + j * 16, make_uint4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]));
         }
       }
     } else {
@@ -417,7 +453,7 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
         const bool here = mbar_wait(&hdr->acc_full[buf], (ch >> 1) & 1, abort_flag, nullptr, 0);
         if (!__all_sync(0xFFFFFFFFu, here)) break;
         tc_fence_after();
-        if (mine) {
+        if (any) {
           // a K range whose last chunk is shorter than the rotation leaves
           // no accumulator out: every k block writes all kAcc of them
 #pragma unroll
@@ -435,35 +471,40 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(&hdr->acc_empty[buf]);
       }
-      // the ring is free once the last chunk's MMAs are complete: every load landed before them
-      if (mine) {
+      if (any && mine) {
 #pragma unroll
         for (int c = 0; c < kHalf; c += 4)
-          *reinterpret_cast<float4*>(dst + c * 4) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+          st_cluster16(dst + c * 4, make_uint4(__float_as_uint(sum[c]), __float_as_uint(sum[c + 1]),
+                                               __float_as_uint(sum[c + 2]), __float_as_uint(sum[c + 3])));
       }
     }
     tc_fence_before();
   }
   __syncwarp();
   // an abort anywhere in the cluster keeps all of it from storing
-  if (S > 1) cluster_sync_all();
-  else __syncthreads();
-  __syncwarp();
-  const bool raised =
-      S == 1 ? *abort_flag != 0 : lane < S && ld_cluster16(smem_u32(const_cast<int*>(abort_flag)), lane).x != 0;
-  const bool ok = !__any_sync(0xFFFFFFFFu, raised);
-  if (!ok && threadIdx.x == 0) record_error(p.status, MOE_ERR_TIMEOUT);
-  if (ok && warp < kDenseEpiWarps) {
-    switch (S) {
-      case 1: join_and_store<KIND, NT, 1>(p, hdr, ring, rank, rows, m0, n0); break;
-      case 2: join_and_store<KIND, NT, 2>(p, hdr, ring, rank, rows, m0, n0); break;
-      case 4: join_and_store<KIND, NT, 4>(p, hdr, ring, rank, rows, m0, n0); break;
-      default: join_and_store<KIND, NT, 8>(p, hdr, ring, rank, rows, m0, n0); break;
-    }
+  if (S > 1) {
+    if (kSent && warp >= kDenseEpiWarps) cluster_wait();
+    __syncthreads();
+    if (threadIdx.x < S)
+      st_cluster4(mapa_rank(smem_u32(const_cast<uint32_t*>(&hdr->raised[rank])), threadIdx.x), *abort_flag != 0);
+    __syncwarp();
+    cluster_sync_all();
+  } else {
+    if (threadIdx.x == 0) hdr->raised[0] = *abort_flag != 0;
+    __syncthreads();
   }
   __syncwarp();
-  if (S > 1) cluster_sync_all();               // no CTA leaves while its shared memory is read
-  else __syncthreads();
+  const bool ok = !__any_sync(0xFFFFFFFFu, lane < S && hdr->raised[lane] != 0);
+  if (!ok && threadIdx.x == 0) record_error(p.status, MOE_ERR_TIMEOUT);
+  if (ok && warp < kDenseEpiWarps) {
+    const int r = static_cast<int>(rank);
+    if (!kSent && S == 1) join_and_store<KIND, NT, false, 1>(p, hdr, staged, slots, r, rows, m0, n0);
+    else if (S == 2) join_and_store<KIND, NT, kSent, 2>(p, hdr, staged, slots, r, rows, m0, n0);
+    else if (S == 4) join_and_store<KIND, NT, kSent, 4>(p, hdr, staged, slots, r, rows, m0, n0);
+    else join_and_store<KIND, NT, kSent, 8>(p, hdr, staged, slots, r, rows, m0, n0);
+  }
+  __syncwarp();
+  if (!kSent && S > 1) cluster_sync_all();  // no CTA leaves while its shared memory is read
   __syncwarp();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, Cfg::kCols);
