@@ -29,7 +29,7 @@ struct Range {
 };
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;
-constexpr int64_t kMaxStride = int64_t(1) << 32;
+constexpr int64_t kMaxStride = int64_t(1) << 31;   // rows x strides x 4 bytes stay below 2^63
 
 // ---------------------------------------------------------------- norm
 constexpr int kNormMaxHidden = 32768;   // 1024 threads x 4 vectors of 8
@@ -141,10 +141,11 @@ struct DensePlan {
 // by cudaOccupancyMaxActiveClusters).
 int cluster_slots(int s, int sms) { return s <= 2 ? sms / s * s : s == 4 ? sms * 132 / 148 : sms * 120 / 148; }
 
-// Shared memory of dense_kernel: the partial sums that a CTA is sent, whether
-// they are (while they are few bytes; dense.cuh has both ways), and what is needed
-// beside the ring (a `block` is a k block's bytes): the header, the 128 rows
-// of x that an MMA reads whatever their number is, and such partials.
+// Shared memory of dense_kernel: the partial sums of a tile; whether a cluster
+// sends them to their owners (while they are few bytes: dense.cuh has both
+// ways); and what lies beside the ring (`block`: a k block's bytes): the
+// header, the 128 rows of x that an MMA reads whatever their number is, and
+// partials that are sent.
 int dense_staging_bytes(int rows, int nt, int splits) {
   return (rows + splits - 1) / splits * splits * (nt * 4 + 16);
 }
@@ -156,6 +157,7 @@ int dense_fixed_bytes(int block, int rows, int nt, int splits) {
   return 1024 + kDenseHeader + dense_behind_bytes(block) +
          (dense_sent(rows, nt, splits) ? dense_staging_bytes(rows, nt, splits) : 0);
 }
+
 // k blocks per stage.  Two while they are small: a wait, a commit and a
 // barrier's arming for every eight MMAs.  Two also for BF16 tiles of 128
 // columns that each have an SM and the whole K axis to themselves (8192 x 256
@@ -169,9 +171,10 @@ int dense_stage_blocks(int kind, int rows, int nt, int splits, int64_t ctas, int
 
 // Tile and K split of dense_kernel by estimated time: whole waves of CTAs,
 // each its share of the k blocks at the slowest of issue, loads and MMAs,
-// plus what a tile costs besides.  The constants are a fit to 370 timings (27
-// sizes, every width and split); over those sizes its choices are within 3 %
-// of the best at the median and 23 % at worst.
+// plus what a tile costs besides.  The constants are a fit to timings of 32
+// sizes, from 1 x 60 x 2048 to 16384 x 128 x 8192 bytes, at every width and
+// split; of 28 sizes timed again it takes the fastest or one within 5 % for 23,
+// within 15 % for the others.
 template <int KIND>
 DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
   constexpr int kWidest = KIND == KIND_I8 ? 256 : 128;
@@ -185,7 +188,8 @@ DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
       const int blk0 = (M >= 128 ? 128 : static_cast<int>((M + 7) / 8 * 8)) + nt;
       const int stage0 = blk0 * 128 * dense_stage_blocks(KIND, blk0 - nt, nt, s, mt0 * n_tiles * s, sms);
       int res = 1;
-      if (mt0 * n_tiles * s > sms && kDenseHalfSmemBytes - dense_fixed_bytes(blk0 * 128, blk0 - nt, nt, s) >= 3 * stage0) res = 2;
+      const int half = kDenseHalfSmemBytes - dense_fixed_bytes(blk0 * 128, blk0 - nt, nt, s);
+      if (mt0 * n_tiles * s > sms && half >= 3 * stage0) res = 2;
       const int64_t slots = int64_t(cluster_slots(s, sms)) * res;
       const int64_t waves = (mt0 * n_tiles * s + slots - 1) / slots;
       int64_t mt = waves * slots / (n_tiles * s);
@@ -489,6 +493,7 @@ moe_status_t moe_router_logits(const moe_problem_t* p, const void* x_bf16, const
   const moe_status_t s = check_problem(p);
   if (s != MOE_OK) return s;
   const int64_t M = p->num_tokens, H = p->hidden;
+  if (H > (int64_t(1) << 29) || M > kMaxRows) return MOE_ERR_UNSUPPORTED;   // a row's bytes are 32-bit coordinates
   if (M == 0) return MOE_OK;
   if (!x_bf16 || !router_weight || !logits || !device_status) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x_bf16) || !aligned16(router_weight) || !aligned(logits, 4) || !aligned(device_status, 4))

@@ -24,13 +24,11 @@
 // the others', and the cluster meets again before any CTA leaves (4096 x 256 x
 // 7168: 24 us against 26).
 //
-// Accumulators.  Consecutive MMAs of one k block go to kAcc different ones:
-// an MMA into the accumulator that its predecessor writes waits for it.  Of
-// BF16 the tensor cores truncate as they add to the accumulator, so a sum's
-// error grows with the number of MMAs behind it (4.4e-6 relative after 256);
-// no accumulator gets more than kChain of them: the epilogue warps then add
+// Of BF16 the tensor cores truncate as they add to the accumulator, so a
+// sum's error grows with the number of MMAs behind it (4.4e-6 relative after
+// 256); no accumulator gets more than 16 of them: the epilogue warps then add
 // it to FP32 registers, rounding to nearest, while the MMAs fill the other
-// half of a double buffer.
+// of two (2.4e-7 at H = 4096).
 //
 // What bounds it: with few rows the stream of w from HBM, which S and NT
 // spread over the SMs; with many rows the tensor cores and the operands'
@@ -140,14 +138,11 @@ __device__ __forceinline__ void st_cluster4(uint32_t addr, uint32_t v) {
 // Shape of one tile's accumulators in TMEM.
 template <int KIND, int NT>
 struct DenseCfg {
-  // independent accumulators that the MMAs of a k block rotate over
-  static constexpr int kAcc = KIND == KIND_I8 ? (NT <= 64 ? 4 : NT == 128 ? 2 : 1) : (NT <= 32 ? 4 : NT == 64 ? 2 : 1);
-  static constexpr int kBufs = KIND == KIND_I8 ? 1 : 2;      // BF16: emptied in turn
-  static constexpr int kChain = 16;                          // BF16: MMAs per accumulator until it is emptied
-  static constexpr int kChunk = KIND == KIND_I8 ? (1 << 30) : kChain * kAcc / 4;   // k blocks per buffer
-  static constexpr int kCols = NT * kAcc * kBufs;
+  static constexpr int kBufs = KIND == KIND_I8 ? 1 : 2;            // accumulators; BF16: emptied in turn
+  static constexpr int kChunk = KIND == KIND_I8 ? (1 << 30) : 4;   // k blocks (of 4 MMAs) until one is emptied
+  static constexpr int kCols = NT * kBufs;
   static constexpr int kPitch = NT * 4 + 16;                 // bytes of a staged row: 16 more spread the banks
-  static_assert(kCols == 128 || kCols == 256, "TMEM columns");
+  static_assert(kCols >= 32 && kCols <= 256, "TMEM columns");
 };
 
 struct DenseHeader {
@@ -371,14 +366,14 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
             tc_fence_after();
           }
           const uint64_t off = (stage * stage_bytes + b * block_bytes) >> 4;
-          const uint32_t d = tmem + buf * Cfg::kAcc * NT;
+          const uint32_t d = tmem + buf * NT;
 #pragma unroll
           for (int kc = 0; kc < 4; ++kc) {
-            const uint32_t acc = in > 0 || kc >= Cfg::kAcc;
+            const uint32_t acc = in > 0 || kc > 0;
             if (KIND == KIND_I8)
-              mma_i8(d + (kc % Cfg::kAcc) * NT, ad0 + off + 2 * kc, bd0 + off + 2 * kc, idesc, acc);
+              mma_i8(d, ad0 + off + 2 * kc, bd0 + off + 2 * kc, idesc, acc);
             else
-              mma_f16(d + (kc % Cfg::kAcc) * NT, ad0 + off + 2 * kc, bd0 + off + 2 * kc, idesc, acc);
+              mma_f16(d, ad0 + off + 2 * kc, bd0 + off + 2 * kc, idesc, acc);
           }
           ++in;
           if (Cfg::kBufs > 1 && (in == Cfg::kChunk || kb + b == kb1 - 1)) {
@@ -431,17 +426,12 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
 #pragma unroll
         for (int c = 0; c < kHalf; c += 16) {
           float v[16];
-          uint32_t s[16];
-#pragma unroll
-          for (int a = 0; a < Cfg::kAcc; ++a) {
-            tmem_ld16(t + a * NT + c, v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              s[j] = a == 0 ? __float_as_uint(v[j]) : add_partial<KIND>(s[j], __float_as_uint(v[j]));
-          }
+          tmem_ld16(t + c, v);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (mine) st_cluster16(dst + c * 4 + j * 16, make_uint4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]));
+            if (mine)
+              st_cluster16(dst + c * 4 + j * 16, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                                            __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
         }
       }
     } else {
@@ -454,17 +444,12 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
         if (!__all_sync(0xFFFFFFFFu, here)) break;
         tc_fence_after();
         if (any) {
-          // a K range whose last chunk is shorter than the rotation leaves
-          // no accumulator out: every k block writes all kAcc of them
 #pragma unroll
-          for (int a = 0; a < Cfg::kAcc; ++a) {
+          for (int c = 0; c < kHalf; c += 16) {
+            float v[16];
+            tmem_ld16(t + buf * NT + c, v);
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 16) {
-              float v[16];
-              tmem_ld16(t + (buf * Cfg::kAcc + a) * NT + c, v);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) sum[c + j] = __fadd_rn(sum[c + j], v[j]);
-            }
+            for (int j = 0; j < 16; ++j) sum[c + j] = __fadd_rn(sum[c + j], v[j]);
           }
         }
         tc_fence_before();

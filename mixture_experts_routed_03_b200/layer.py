@@ -42,6 +42,8 @@ def _expect(name, t, dtypes, shape, device=None):
         raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} {tuple(shape)}, got {got}")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be dense")
+    if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows that overlap (an expanded tensor?) are not taken")
     if device is not None and (t.device.type != device.type or device.index not in (None, t.device.index)):
         raise ValueError(f"{name} is on {t.device}, not on {device}")
 
@@ -80,6 +82,8 @@ def rmsnorm_quantize(x, weight, residual=None, format="bf16", eps=1e-6, static_s
         _expect("residual", residual, (torch.bfloat16, torch.float32), (M, H), dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
+    if residual_out is not None:
+        _expect("residual_out", residual_out, (residual.dtype,), (M, H), dev)
     if static_scale is not None:
         _expect("static_scale", static_scale, (torch.float32,), (1,), dev)
     if format not in api.NORM_FORMATS:
@@ -87,8 +91,6 @@ def rmsnorm_quantize(x, weight, residual=None, format="bf16", eps=1e-6, static_s
     with _on(dev, stream):
         if residual is not None and residual_out is None:
             residual_out = torch.empty((M, H), dtype=residual.dtype, device=dev)
-        elif residual is not None:
-            _expect("residual_out", residual_out, (residual.dtype,), (M, H), dev)
         y = torch.empty((M, H), dtype=torch.bfloat16, device=dev) if norm or format == "bf16" else None
         codes = scales = None
         if format != "bf16":

@@ -67,7 +67,7 @@ def _norm(lib, problem=None, **kw):
     (dict(residual_fp32=2), BAD), (dict(weight_fp32=-1), BAD),
     (dict(x_stride=248), BAD), (dict(x_stride=260), BAD), (dict(x_stride=-256), BAD),
     (dict(residual_in_stride=252), BAD), (dict(residual_out_stride=260), BAD),
-    (dict(residual_out_stride=258, residual_fp32=1), BAD),
+    (dict(residual_out_stride=258, residual_fp32=1), BAD), (dict(x_stride=(1 << 31) + 8), BAD),
 ])
 def test_norm_problem_refused(lib, kw, code):
     d = dict(num_tokens=4, hidden=256, format="fp8")
@@ -123,6 +123,7 @@ def test_router_arguments_refused(lib):
         assert call(**kw) == BAD, kw
     assert call(prob=api.problem(4, 300, 128, 8, 2)) == BAD
     assert call(prob=api.problem(4, 256, 128, 2000, 2)) == UNSUPPORTED
+    assert call(prob=api.problem(4, (1 << 29) + 256, 128, 1, 1)) == UNSUPPORTED
     assert call(prob=api.problem(0, 256, 128, 8, 2), x=None, w=None, logits=None, status=None) == OK
 
 
@@ -140,7 +141,7 @@ def _int8(lib, problem=None, **kw):
     (dict(num_tokens=-1), BAD), (dict(in_features=0), BAD), (dict(out_features=0), BAD), (dict(out_fp32=2), BAD),
     (dict(in_features=65), BAD),                         # rows of 65 bytes cannot be loaded: pad them
     (dict(x_stride=48), BAD), (dict(x_stride=72), BAD), (dict(w_stride=63), BAD), (dict(out_stride=7), BAD),
-    (dict(x_stride=-64), BAD),
+    (dict(x_stride=-64), BAD), (dict(x_stride=(1 << 31) + 16), BAD), (dict(out_stride=(1 << 31) + 1), BAD),
     (dict(in_features=131072), UNSUPPORTED), (dict(num_tokens=(1 << 30) + 1), UNSUPPORTED),
 ])
 def test_int8_problem_refused(lib, kw, code):
@@ -174,7 +175,9 @@ def test_python_checks_raise_before_any_call():
                      ((x[0], w), {}), ((x.t(), w), {}), ((x, w), dict(residual=x[:2])),
                      ((x, w), dict(residual_out=x)), ((x, w), dict(residual=x.double())),
                      ((x, w), dict(format="nvfp4")), ((x, w), dict(static_scale=w[:1])),
-                     (([1.0], w), {})):
+                     (([1.0], w), {}), ((x[:1].expand(4, 256), w), {}),
+                     ((x, w), dict(residual=x[:1].expand(4, 256))),
+                     ((x, w), dict(residual=x, residual_out=x[:1].expand(4, 256)))):
         with pytest.raises(ValueError):
             layer.rmsnorm_quantize(*args, **kw)
     i = torch.zeros((8, 64), dtype=torch.int8)
@@ -183,7 +186,7 @@ def test_python_checks_raise_before_any_call():
         with pytest.raises(ValueError):
             layer.Int8Linear(*args)
     lin = layer.Int8Linear(i, s)
-    for args, kw in (((i[:, :32], s), {}), ((i, s[:4]), {}), ((i[0], s), {}), ((i.float(), s), {}),
+    for args, kw in (((i[:1].expand(8, 64), s), {}), ((i[:, :32], s), {}), ((i, s[:4]), {}), ((i[0], s), {}), ((i.float(), s), {}),
                      ((i, s), dict(out_dtype=torch.float16)), ((i, s), dict(out=torch.zeros((8, 7))))):
         with pytest.raises(ValueError):
             lin.forward(*args, **kw)
