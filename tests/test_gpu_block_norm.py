@@ -276,3 +276,34 @@ def test_the_same_bits_every_time():
     # and a token's result does not depend on its neighbours
     one = layer.rmsnorm_quantize(x[5:6], w, r[5:6], "int8", norm=True)
     assert all(torch.equal(p[5:6].view(torch.uint8), q.view(torch.uint8)) for p, q in zip(a, one))
+
+
+@pytest.mark.parametrize("fmt,H", [("int8", 16384), ("mxfp8", 16384), ("fp8", 512)])
+def test_offsets_past_32_bits(fmt, H):
+    M = (1 << 31) // H + 5
+    x, _, w, ss = _inputs(4, H, None, seed=18)
+    rows = [0, 7, M - 2, M - 1]
+    big = torch.zeros((M, H), dtype=torch.bfloat16, device=DEV)
+    big[rows] = x
+    out = layer.rmsnorm_quantize(big, w, None, fmt)
+    check(type(out)(*[None if t is None else t[rows] for t in out]), x, None, w, ss, fmt, 1e-6)
+    assert not (out.codes[100:200].view(torch.uint8) & 0x7F).any()
+
+
+def test_residual_of_the_other_rows_is_untouched_in_place():
+    """In place on a slice of a longer stream: the tokens before and behind keep theirs."""
+    x, r, w, ss = _inputs(40, 1024, "bf16", seed=19)
+    kept = r.clone()
+    part = r[8:30]
+    out = layer.rmsnorm_quantize(x[8:30], w, part, "fp8", residual_out=part)
+    assert torch.equal(r[:8], kept[:8]) and torch.equal(r[30:], kept[30:])
+    check(out, x[8:30], kept[8:30], w, ss, "fp8", 1e-6)
+
+
+def test_overlapping_arguments_are_refused():
+    x, r, w, _ = _inputs(8, 512, "bf16", seed=20)
+    with pytest.raises(api.MoEError):
+        layer.rmsnorm_quantize(x, w, r, "fp8", residual_out=x)
+    longer = torch.cat([r, r[:1]])
+    with pytest.raises(api.MoEError):
+        layer.rmsnorm_quantize(x, w, longer[:8], "fp8", residual_out=longer[1:])

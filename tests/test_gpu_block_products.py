@@ -200,3 +200,64 @@ def test_router_row_of_nan_stays_alone():
     assert torch.isnan(out[4]).all()
     keep = [0, 1, 2, 3, 5, 6, 7, 8]
     _check_logits(out[keep], x[keep], w)
+
+
+# ------------------------------------------------------------------ offsets past 32 bits, other work beside
+
+def test_int8_output_past_32_bit_offsets():
+    M, N, K = 270001, 8200, 16          # 2.2e9 outputs
+    g = torch.Generator().manual_seed(11)
+    rows = [0, 1, 262143, 262144, M - 2, M - 1]
+    few, w = _codes((len(rows), K), g), _codes((N, K), g)
+    ws = torch.rand((N,), generator=g)
+    x = torch.zeros((M, K), dtype=torch.int8, device=DEV)
+    xs = torch.ones((M,), device=DEV)
+    x[rows] = few.to(DEV)
+    out = layer.Int8Linear(w.to(DEV), ws.to(DEV)).forward(x, xs)
+    _check(out[rows], (few, torch.ones(len(rows)), w, ws, None), False)
+    assert not out[2:262143].any()
+
+
+def test_router_rows_past_32_bit_offsets():
+    M, E, H = 300003, 8, 8192           # 2.4e9 activations
+    x, w = _router(4, E, H, seed=12)
+    big = torch.zeros((M, H), dtype=torch.bfloat16, device=DEV)
+    rows = [0, 262144, M - 2, M - 1]
+    big[rows] = x.to(DEV)
+    out = torch.empty((M, E), device=DEV)
+    status = _status()
+    api.router_logits(api.problem(M, H, 128, E, 1), big, w.to(DEV), out, status)
+    _check_logits(out[rows], x, w)
+    assert int(status.item()) == api.MOE_OK
+
+
+@pytest.mark.parametrize("M", [1, 2, 8, 40, 700, 3000])
+def test_products_beside_each_other_on_two_streams(M):
+    """Both kinds at once, and of one kind two calls of different sizes: the
+    streams share the SMs, their tensor memory and nothing else."""
+    case = _case(M, 1200, 1024, seed=20 + M)
+    lin = layer.Int8Linear(case[2].to(DEV), case[3].to(DEV), case[4].to(DEV))
+    x, xs = case[0].to(DEV), case[1].to(DEV)
+    rx, rw = _router(M, 96, 2048, seed=21 + M)
+    gx, gw = rx.to(DEV), rw.to(DEV)
+    logits, status = torch.empty((M, 96), device=DEV), _status()
+    p = api.problem(M, 2048, 128, 96, 1)
+    a, b = torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        out = lin.forward(x, xs, stream=a)
+        api.router_logits(p, gx, gw, logits, status, stream=b)
+        small = lin.forward(x[:1], xs[:1], stream=b)
+    torch.cuda.synchronize()
+    _check(out, case, True)
+    _check(small, (case[0][:1], case[1][:1]) + case[2:], True)
+    _check_logits(logits, rx, rw)
+    lin.check_status()
+    assert int(status.item()) == api.MOE_OK
+
+
+def test_overlapping_arguments_are_refused():
+    buf = torch.zeros((64, 256), dtype=torch.int8, device=DEV)
+    lin = layer.Int8Linear(torch.ones((16, 64), dtype=torch.int8, device=DEV), torch.ones(16, device=DEV))
+    with pytest.raises(api.MoEError):
+        lin.forward(buf[:, :64], torch.ones(64, device=DEV), out=buf.view(torch.bfloat16)[:, 64:80])
