@@ -55,7 +55,9 @@ def _check(got, case, bias):
 SHAPES = [(1, 1, 1), (1, 32, 128), (1, 1001, 4096), (2, 33, 100), (7, 31, 16), (8, 257, 1040), (9, 64, 144),
           (31, 255, 2048), (33, 96, 384), (64, 1536, 2048), (127, 130, 512), (128, 128, 128), (129, 300, 257),
           (200, 1, 640), (300, 1001, 1040), (513, 768, 2048), (1, 4096, 7168), (3000, 520, 256), (2500, 2500, 144),
-          (1300, 1600, 272), (5000, 700, 400), (9473, 257, 130), (2400, 2104, 16), (12000, 129, 1040), (1281, 2305, 2048)]
+          (1300, 1600, 272), (5000, 700, 400), (9473, 257, 130), (2400, 2104, 16), (12000, 129, 1040), (1281, 2305, 2048),
+          (2, 1500, 2048), (2, 3000, 2050), (1, 500, 8192), (16, 4096, 7168), (64, 4096, 7168), (128, 4096, 7168),
+          (256, 4096, 7168), (777, 7168, 2048), (2048, 4096, 512), (40, 64, 8192), (150, 200, 16384), (1000, 100, 4096)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -172,7 +174,9 @@ def _check_logits(got, x, w):
 @pytest.mark.parametrize("M,E,H", [(1, 1, 256), (1, 256, 7168), (3, 8, 256), (17, 60, 2048), (64, 256, 7168),
                                    (127, 65, 512), (130, 128, 4096), (777, 60, 2048), (300, 1024, 256),
                                    (4100, 33, 512), (1500, 1001, 768), (9000, 128, 1024), (16384, 60, 512),
-                                   (20001, 300, 768), (3000, 256, 2048), (12345, 64, 4096)])
+                                   (20001, 300, 768), (3000, 256, 2048), (12345, 64, 4096), (2, 700, 2048),
+                                   (4, 256, 7168), (5, 60, 2048), (8, 1000, 1024), (9, 256, 7168), (300, 256, 7168),
+                                   (1000, 128, 4096), (4096, 256, 7168), (2000, 60, 2048), (3000, 20, 7168)])
 def test_router_logits(M, E, H):
     x, w = _router(M, E, H, seed=M)
     buf = torch.full((M + 1, E), 3.0, device=DEV)
