@@ -141,22 +141,9 @@ struct DensePlan {
 // by cudaOccupancyMaxActiveClusters).
 int cluster_slots(int s, int sms) { return s <= 2 ? sms / s * s : s == 4 ? sms * 132 / 148 : sms * 120 / 148; }
 
-// Shared memory of dense_kernel: the partial sums of a tile; whether a cluster
-// sends them to their owners (while they are few bytes: dense.cuh has both
-// ways); and what lies beside the ring (`block`: a k block's bytes): the
-// header, the 128 rows of x that an MMA reads whatever their number is, and
-// partials that are sent.
-int dense_staging_bytes(int rows, int nt, int splits) {
-  return (rows + splits - 1) / splits * splits * (nt * 4 + 16);
-}
-bool dense_sent(int rows, int nt, int splits) {
-  return splits > 1 && nt <= 64 && dense_staging_bytes(rows, nt, splits) <= 20 * 1024;
-}
-int dense_behind_bytes(int block) { return block < 128 * 128 ? 128 * 128 - block : 0; }
-int dense_fixed_bytes(int block, int rows, int nt, int splits) {
-  return 1024 + kDenseHeader + dense_behind_bytes(block) +
-         (dense_sent(rows, nt, splits) ? dense_staging_bytes(rows, nt, splits) : 0);
-}
+// Shared memory of dense_kernel beside its ring (`block`: a k block's bytes):
+// the header and the 128 rows of x that an MMA reads whatever their number is.
+int dense_fixed_bytes(int block) { return 1024 + kDenseHeader + (block < 128 * 128 ? 128 * 128 - block : 0); }
 
 // k blocks per stage.  Two while they are small: a wait, a commit and a
 // barrier's arming for every eight MMAs.  Two also for BF16 tiles of 128
@@ -188,7 +175,7 @@ DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
       const int blk0 = (M >= 128 ? 128 : static_cast<int>((M + 7) / 8 * 8)) + nt;
       const int stage0 = blk0 * 128 * dense_stage_blocks(KIND, blk0 - nt, nt, s, mt0 * n_tiles * s, sms);
       int res = 1;
-      const int half = kDenseHalfSmemBytes - dense_fixed_bytes(blk0 * 128, blk0 - nt, nt, s);
+      const int half = kDenseHalfSmemBytes - dense_fixed_bytes(blk0 * 128);
       if (mt0 * n_tiles * s > sms && half >= 3 * stage0) res = 2;
       const int64_t slots = int64_t(cluster_slots(s, sms)) * res;
       const int64_t waves = (mt0 * n_tiles * s + slots - 1) / slots;
@@ -238,7 +225,7 @@ cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap&
   p.stage_blocks = dense_stage_blocks(KIND, p.tile_rows, NT, p.splits, grid, sms);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const int block = (p.tile_rows + NT) * 128, stage = block * p.stage_blocks;
-  const int fixed = dense_fixed_bytes(block, p.tile_rows, NT, p.splits);
+  const int fixed = dense_fixed_bytes(block);
   // two CTAs an SM where there are more than SMs and a ring of three stages
   // fits in half of the shared memory
   int room = kDenseSmemBytes - fixed;
@@ -248,10 +235,9 @@ cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap&
   if (p.stages > kDenseMaxStages) p.stages = kDenseMaxStages;
   const int per_cta = ((p.k_blocks + p.splits - 1) / p.splits + p.stage_blocks - 1) / p.stage_blocks;
   if (p.stages > per_cta) p.stages = per_cta;
-  p.ring_bytes = p.stages * stage + dense_behind_bytes(block);
-  const bool sent = dense_sent(p.tile_rows, NT, p.splits);
-  const int staging = dense_staging_bytes(p.tile_rows, NT, p.splits);
-  int smem = 1024 + kDenseHeader + (sent ? p.ring_bytes + staging : p.ring_bytes > staging ? p.ring_bytes : staging);
+  const int ring = p.stages * stage + fixed - 1024 - kDenseHeader;
+  const int staging = (p.tile_rows + 31) / 32 * 32 * (NT * 4 + 16);   // the partial tile, in the ring
+  int smem = 1024 + kDenseHeader + (ring > staging ? ring : staging);
   if (smem < kDenseMinSmemBytes) smem = kDenseMinSmemBytes;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -267,8 +253,7 @@ cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap&
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  if (NT <= 64 && sent) return cudaLaunchKernelEx(&cfg, dense_kernel<KIND, NT <= 64 ? NT : 64, true>, p, tx, tw);
-  return cudaLaunchKernelEx(&cfg, dense_kernel<KIND, NT, false>, p, tx, tw);
+  return cudaLaunchKernelEx(&cfg, dense_kernel<KIND, NT>, p, tx, tw);
 }
 
 template <int KIND, int MB, int R, int D>
@@ -334,7 +319,9 @@ moe_status_t run_pair(const DenseArgs& p, int nt, const void* x, const void* w, 
   a.out = p.out;
   a.out_stride = p.out_stride;
   const int per16 = p.out_fp32 ? 4 : 8;
-  a.vec = aligned16(p.out) && p.out_stride % per16 == 0;
+  // a TMA store writes whole 16-byte pieces: rows that end within one would
+  // lose what lies behind them
+  a.vec = aligned16(p.out) && p.out_stride % per16 == 0 && p.N % per16 == 0;
   a.status = p.status;
   a.m_tiles = static_cast<int>((p.M + 255) / 256);
   a.n_tiles = (p.N + nt - 1) / nt;
@@ -380,19 +367,17 @@ moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_byt
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-template <int KIND, int NT, bool kSent>
+template <int KIND, int NT>
 cudaError_t set_dense_attr() {
-  return cudaFuncSetAttribute(dense_kernel<KIND, NT, kSent>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmemBytes);
+  return cudaFuncSetAttribute(dense_kernel<KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDenseSmemBytes);
 }
 
 template <int KIND>
 cudaError_t set_dense_attrs() {
-  cudaError_t e = set_dense_attr<KIND, 32, true>();
-  if (e == cudaSuccess) e = set_dense_attr<KIND, 64, true>();
-  if (e == cudaSuccess) e = set_dense_attr<KIND, 32, false>();
-  if (e == cudaSuccess) e = set_dense_attr<KIND, 64, false>();
-  if (e == cudaSuccess) e = set_dense_attr<KIND, 128, false>();
-  if (e == cudaSuccess && KIND == KIND_I8) e = set_dense_attr<KIND_I8, 256, false>();
+  cudaError_t e = set_dense_attr<KIND, 32>();
+  if (e == cudaSuccess) e = set_dense_attr<KIND, 64>();
+  if (e == cudaSuccess) e = set_dense_attr<KIND, 128>();
+  if (e == cudaSuccess && KIND == KIND_I8) e = set_dense_attr<KIND_I8, 256>();
   return e;
 }
 

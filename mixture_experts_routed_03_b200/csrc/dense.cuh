@@ -13,16 +13,15 @@
 // swizzle's 8), since the accumulator rows of what lies behind them are never
 // read -- so the row tiles are cut to fill the last wave of SMs.  Warp 8 loads,
 // warp 9 issues the MMAs into TMEM, warps 0-7 (two per 32-lane TMEM quarter,
-// one per half of the columns) take the sums out.  The CTAs of a cluster share
-// out the tile's rows (row r belongs to rank r mod S): every owner sums its
-// rows over the ranks in their order (so results do not depend on timing; no
-// workspace, no atomics), scales and stores them.  The partials cross through
-// distributed shared memory, in one of two ways.  Few bytes are written into
-// the owner's memory, beside its ring, and the cluster meets once (64 x 256 x
-// 7168 BF16: 7.3 us against 7.9 the other way).  Otherwise each CTA leaves its
-// partial tile in its own ring, free by then, the cluster meets, owners read
-// the others', and the cluster meets again before any CTA leaves (4096 x 256 x
-// 7168: 24 us against 26).
+// one per half of the columns) take the sums out.  Then each CTA leaves its
+// partial tile in its own shared memory, the cluster meets, and the CTAs share
+// out the tile's elements: each is summed over the ranks in their order through
+// distributed shared memory (so results do not depend on timing; no workspace,
+// no atomics), scaled and stored; the cluster meets again before any CTA
+// leaves.  (Partials written into their owners' memory instead, with nothing
+// remote after the one meeting, took half a microsecond less at 64 x 256 x 7168
+// but faulted now and then where two CTAs shared an SM; the cause was not found
+// by reading, so it is not done.)
 //
 // Of BF16 the tensor cores truncate as they add to the accumulator, so a
 // sum's error grows with the number of MMAs behind it (4.4e-6 relative after
@@ -69,7 +68,6 @@ struct DenseArgs {
   int tile_rows;           // output rows per tile: a multiple of 8, at most 128
   int stages;
   int stage_blocks;        // k blocks per stage, 1 or 2
-  int ring_bytes;
   int out_fp32;
   int vec;                 // outputs may be stored four at a time
   const float* x_scale;    // [M] (KIND_I8)
@@ -116,6 +114,7 @@ __device__ __forceinline__ uint32_t mapa_rank(uint32_t saddr, uint32_t rank) {
   return r;
 }
 
+// 16 bytes at an address of the cluster.
 __device__ __forceinline__ uint4 ld_cluster16(uint32_t addr) {
   uint4 v;
   // volatile keeps it behind the cluster's barrier; without a memory clobber
@@ -124,15 +123,6 @@ __device__ __forceinline__ uint4 ld_cluster16(uint32_t addr) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(addr));
   return v;
-}
-
-__device__ __forceinline__ void st_cluster16(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
-__device__ __forceinline__ void st_cluster4(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Shape of one tile's accumulators in TMEM.
@@ -150,8 +140,7 @@ struct DenseHeader {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;                            // after an abort: the MMAs issued are complete
   uint32_t tmem;
-  alignas(16) volatile int abort_flag[4];    // raised, wait limit (0: the default)
-  volatile uint32_t raised[8];               // the ranks' abort flags at the join
+  alignas(16) volatile int abort_flag[4];    // raised, wait limit (0: the default); read 16 bytes at a time
   alignas(16) float xs[128], ws[256], bias[256];   // the tile's scales (KIND_I8)
 };
 static_assert(sizeof(DenseHeader) <= kDenseHeader, "header");
@@ -204,45 +193,43 @@ __device__ __forceinline__ void store_out4(const DenseArgs& p, int64_t m, int c,
   }
 }
 
-// Sums this rank's rows (rank, rank + S, ...) over the S ranks' partials, in
-// rank order, and stores them.  Rank q's partial of row r is row q * slots + r
-// / S of this CTA's staging if it was sent here, else row r of rank q's.  A thread keeps its column group throughout: the step
-// from one element to the next is a multiple of the groups of a row.
-template <int KIND, int NT, bool kSent, int S>
+// Sums the tile's elements over the S ranks' staged partials, in rank order,
+// and stores this rank's share.  A thread keeps its column group throughout:
+// the step from one element to the next is a multiple of the groups of a row.
+template <int KIND, int NT, int S>
 __device__ __forceinline__ void join_and_store(const DenseArgs& p, const DenseHeader* hdr, const uint8_t* staged,
-                                               int slots, int rank, int rows, int64_t m0, int n0) {
+                                               uint32_t rank, int rows, int64_t m0, int n0) {
   constexpr int kGroups = NT / 4;
   constexpr int kPitch = DenseCfg<KIND, NT>::kPitch;
-  constexpr int kU = S <= 2 ? 4 : 2;            // rows in flight per thread
-  constexpr int kRowStep = kDenseEpiThreads / kGroups;
-  const int c = (threadIdx.x % kGroups) * 4;
+  constexpr int kU = S == 1 ? 4 : 2;            // rows in flight per thread
+  constexpr int kRowStep = S * kDenseEpiThreads / kGroups;
+  const int g0 = static_cast<int>(rank) * kDenseEpiThreads + threadIdx.x;
+  const int c = (g0 % kGroups) * 4;
   if (n0 + c >= p.N) return;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f), b = w;
   if (KIND == KIND_I8) {
     w = *reinterpret_cast<const float4*>(hdr->ws + c);
     b = *reinterpret_cast<const float4*>(hdr->bias + c);
   }
-  const int own = (rows - rank + S - 1) / S;    // rows of this rank
   const uint32_t base = smem_u32(staged) + c * 4;
-  for (int i0 = threadIdx.x / kGroups; i0 < own; i0 += kU * kRowStep) {
+  for (int r0 = g0 / kGroups; r0 < rows; r0 += kU * kRowStep) {
     uint4 v[kU][S];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int i = i0 + u * kRowStep;
-      if (i >= own) continue;
+      const int r = r0 + u * kRowStep;
+      if (r >= rows) continue;
 #pragma unroll
       for (int q = 0; q < S; ++q) {
         if (S == 1)
-          v[u][q] = *reinterpret_cast<const uint4*>(staged + i * kPitch + c * 4);
+          v[u][q] = *reinterpret_cast<const uint4*>(staged + r * kPitch + c * 4);
         else
-          v[u][q] = ld_cluster16(kSent ? base + (q * slots + i) * kPitch
-                                          : mapa_rank(base + (i * S + rank) * kPitch, q));
+          v[u][q] = ld_cluster16(mapa_rank(base + r * kPitch, q));
       }
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int i = i0 + u * kRowStep;
-      if (i >= own) continue;
+      const int r = r0 + u * kRowStep;
+      if (r >= rows) continue;
       uint4 s = v[u][0];
 #pragma unroll
       for (int q = 1; q < S; ++q) {
@@ -251,14 +238,12 @@ __device__ __forceinline__ void join_and_store(const DenseArgs& p, const DenseHe
         s.z = add_partial<KIND>(s.z, v[u][q].z);
         s.w = add_partial<KIND>(s.w, v[u][q].w);
       }
-      const int r = i * S + rank;
       store_out4<KIND>(p, m0 + r, n0 + c, s, KIND == KIND_I8 ? hdr->xs[r] : 0.0f, w, b);
     }
   }
 }
 
-// kSent: the partials of a cluster (S > 1) are sent to their owners.
-template <int KIND, int NT, bool kSent>
+template <int KIND, int NT>
 __global__ void __launch_bounds__(kDenseThreads, 2)
     dense_kernel(const __grid_constant__ DenseArgs p, const __grid_constant__ CUtensorMap tx,
                  const __grid_constant__ CUtensorMap tw) {
@@ -268,8 +253,6 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
   DenseHeader* hdr = reinterpret_cast<DenseHeader*>(smem);
   volatile int* abort_flag = hdr->abort_flag;
   uint8_t* ring = smem + kDenseHeader;
-  // partials: sent ones beside the ring, which may still be in use when they come
-  uint8_t* staged = ring + (kSent ? p.ring_bytes : 0);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -310,9 +293,6 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = hdr->tmem;
-  // the CTAs of a cluster are there before any of them writes into another
-  if (kSent) cluster_arrive();
-  const int slots = (p.tile_rows + S - 1) / S;
 
   if (warp == 8) {
     if (elect_one()) {
@@ -384,7 +364,9 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
           }
         }
         if (!go) break;
-        mma_commit(&hdr->empty[stage]);
+        // only where a load waits for the stage: a commit's arrival comes on
+        // its own time, and one that nothing waits for could find the CTA gone
+        if (kb + p.stages * p.stage_blocks < kb1) mma_commit(&hdr->empty[stage]);
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
@@ -412,26 +394,21 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t t = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kHalf;
     const int chunks = (kb1 - kb0 + Cfg::kChunk - 1) / Cfg::kChunk;
-    const int row = quarter * 32 + lane;
-    const uint32_t at = smem_u32(staged) + (kSent ? rank * slots + row / S : row) * Cfg::kPitch + half * kHalf * 4;
-    const uint32_t dst = kSent ? mapa_rank(at, row % S) : at;
-    if (kSent) cluster_wait();
-    const bool mine = row < p.tile_rows;
-    const bool any = quarter * 32 < rows;
+    const bool mine = quarter * 32 < rows;
+    uint8_t* dst = ring + (quarter * 32 + lane) * Cfg::kPitch + half * kHalf * 4;
     if (Cfg::kBufs == 1) {
       mbar_wait(&hdr->acc_full[0], 0, abort_flag, nullptr, 0);
       __syncwarp();                            // tcgen05.ld wants the warp together
       tc_fence_after();
-      if (any) {
+      if (mine) {
 #pragma unroll
         for (int c = 0; c < kHalf; c += 16) {
           float v[16];
           tmem_ld16(t + c, v);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (mine)
-              st_cluster16(dst + c * 4 + j * 16, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                                            __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+            *reinterpret_cast<float4*>(dst + c * 4 + j * 16) =
+                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
       }
     } else {
@@ -443,7 +420,7 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
         const bool here = mbar_wait(&hdr->acc_full[buf], (ch >> 1) & 1, abort_flag, nullptr, 0);
         if (!__all_sync(0xFFFFFFFFu, here)) break;
         tc_fence_after();
-        if (any) {
+        if (mine) {
 #pragma unroll
           for (int c = 0; c < kHalf; c += 16) {
             float v[16];
@@ -456,40 +433,35 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(&hdr->acc_empty[buf]);
       }
-      if (any && mine) {
+      // the ring is free once the last chunk's MMAs are complete: every load landed before them
+      if (mine) {
 #pragma unroll
         for (int c = 0; c < kHalf; c += 4)
-          st_cluster16(dst + c * 4, make_uint4(__float_as_uint(sum[c]), __float_as_uint(sum[c + 1]),
-                                               __float_as_uint(sum[c + 2]), __float_as_uint(sum[c + 3])));
+          *reinterpret_cast<float4*>(dst + c * 4) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
       }
     }
     tc_fence_before();
   }
   __syncwarp();
   // an abort anywhere in the cluster keeps all of it from storing
-  if (S > 1) {
-    if (kSent && warp >= kDenseEpiWarps) cluster_wait();
-    __syncthreads();
-    if (threadIdx.x < S)
-      st_cluster4(mapa_rank(smem_u32(const_cast<uint32_t*>(&hdr->raised[rank])), threadIdx.x), *abort_flag != 0);
-    __syncwarp();
-    cluster_sync_all();
-  } else {
-    if (threadIdx.x == 0) hdr->raised[0] = *abort_flag != 0;
-    __syncthreads();
-  }
+  if (S > 1) cluster_sync_all();
+  else __syncthreads();
   __syncwarp();
-  const bool ok = !__any_sync(0xFFFFFFFFu, lane < S && hdr->raised[lane] != 0);
+  const uint32_t flag = smem_u32(const_cast<int*>(abort_flag));
+  const bool raised = S == 1 ? *abort_flag != 0 : lane < S && ld_cluster16(mapa_rank(flag, lane)).x != 0;
+  const bool ok = !__any_sync(0xFFFFFFFFu, raised);
   if (!ok && threadIdx.x == 0) record_error(p.status, MOE_ERR_TIMEOUT);
   if (ok && warp < kDenseEpiWarps) {
-    const int r = static_cast<int>(rank);
-    if (!kSent && S == 1) join_and_store<KIND, NT, false, 1>(p, hdr, staged, slots, r, rows, m0, n0);
-    else if (S == 2) join_and_store<KIND, NT, kSent, 2>(p, hdr, staged, slots, r, rows, m0, n0);
-    else if (S == 4) join_and_store<KIND, NT, kSent, 4>(p, hdr, staged, slots, r, rows, m0, n0);
-    else join_and_store<KIND, NT, kSent, 8>(p, hdr, staged, slots, r, rows, m0, n0);
+    switch (S) {
+      case 1: join_and_store<KIND, NT, 1>(p, hdr, ring, rank, rows, m0, n0); break;
+      case 2: join_and_store<KIND, NT, 2>(p, hdr, ring, rank, rows, m0, n0); break;
+      case 4: join_and_store<KIND, NT, 4>(p, hdr, ring, rank, rows, m0, n0); break;
+      default: join_and_store<KIND, NT, 8>(p, hdr, ring, rank, rows, m0, n0); break;
+    }
   }
   __syncwarp();
-  if (!kSent && S > 1) cluster_sync_all();  // no CTA leaves while its shared memory is read
+  if (S > 1) cluster_sync_all();               // no CTA leaves while its shared memory is read
+  else __syncthreads();
   __syncwarp();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, Cfg::kCols);

@@ -11,8 +11,8 @@
 // of two accumulators, scale, round and store them while the MMAs fill the
 // other: 128 bytes of 32 rows at a time, through shared memory and a TMA
 // store (with plain stores of a thread's own row the epilogue of a tile took
-// longer than its MMAs at K = 2048).  Outputs whose rows are not 16-byte
-// aligned are stored element by element.
+// longer than its MMAs at K = 2048).  Outputs whose rows do not begin
+// and end on 16-byte boundaries are turned around in shared memory instead.
 //
 // What bounds it: the tensor cores while a tile's K axis is long; the waves
 // of tiles over the 74 pairs when there are few.
@@ -39,7 +39,7 @@ struct PairArgs {
   const float* bias;
   void* out;
   int64_t out_stride;
-  int vec;                             // rows of out are 16-byte aligned: stored by TMA
+  int vec;                             // rows of out are whole 16-byte pieces: stored by TMA
   int* status;
 };
 
@@ -250,6 +250,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
       int buf = 0;
       uint32_t buf_phase = 1;
       bool go = true;
+      // k blocks of this pair's tiles from here on
+      int64_t ahead = pair < tiles ? (static_cast<int64_t>(tiles - pair - 1) / pairs + 1) * p.k_blocks : 0;
       for (int t = pair; t < tiles && go; t += pairs) {
         go = mbar_wait(&hdr->acc_empty[buf], buf_phase, abort_flag, nullptr, 0);
         if (!go) break;
@@ -263,7 +265,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
 #pragma unroll
           for (int kc = 0; kc < 4; ++kc)
             mma_i8_pair(d, ad0 + off + 2 * kc, bd0 + off + 2 * kc, idesc, kb > 0 || kc > 0);
-          mma_commit_pair(&hdr->empty[stage]);
+          // only where a load waits for the stage (dense.cuh)
+          if (--ahead >= ST) mma_commit_pair(&hdr->empty[stage]);
           if (++stage == ST) {
             stage = 0;
             phase ^= 1u;

@@ -76,7 +76,8 @@ def test_int8_product_bit_for_bit(M, N, K):
 
 
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("M,N,stride", [(5, 40, 48), (140, 129, 131), (140, 128, 132)])
+@pytest.mark.parametrize("M,N,stride", [(5, 40, 48), (140, 129, 131), (140, 128, 132), (2, 30, 32), (4139, 1454, 1456),
+                                        (2600, 2052, 2064), (3001, 2050, 2056)])
 def test_int8_output_rows_apart_and_nothing_else_written(out_dtype, M, N, stride):
     case = _case(M, N, 256, seed=stride)
     buf = torch.full((M + 2, stride), 5.0, dtype=out_dtype, device=DEV)
@@ -184,6 +185,45 @@ def test_router_logits(M, E, H):
     api.router_logits(api.problem(M, H, 128, E, 1), x.to(DEV), w.to(DEV), buf, status)
     _check_logits(buf[:M], x, w)
     assert (buf[M] == 3).all() and int(status.item()) == api.MOE_OK
+
+
+def test_products_of_many_shapes_one_after_the_other():
+    """Calls of changing shapes back to back, two of each: nothing of one may reach the next."""
+    import math
+    import random
+    rng = random.Random(5)
+
+    def spread(lo, hi):
+        return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+    status = _status()
+    for _ in range(400):
+        M, N, K = spread(1, 3000), spread(1, 1500), spread(1, 5000)
+        if M * N * K > 2e9:
+            continue
+        if rng.random() < 0.5:
+            E, H = min(N, 1024), 256 * max(1, K // 256)
+            x = torch.randn((M, H), device=DEV).to(torch.bfloat16)
+            w = torch.randn((E, H), device=DEV).to(torch.bfloat16)
+            outs = [torch.full((M + 1, E), 7.0, device=DEV) for _ in range(2)]
+            for o in outs:
+                api.router_logits(api.problem(M, H, 128, E, 1), x, w, o, status)
+            want, size = x.double() @ w.double().t(), x.double().abs() @ w.double().abs().t()
+            assert ((outs[0][:M].double() - want).abs() <= (H / 16 + 24) * 2.0 ** -23 * size).all(), (M, E, H)
+            assert torch.equal(outs[0], outs[1]) and (outs[0][M] == 7).all(), (M, E, H)
+        else:
+            stride, os = -(-K // 16) * 16 + 16 * rng.randrange(3), N + rng.randrange(9)
+            x = torch.randint(-128, 128, (M, stride), device=DEV, dtype=torch.int32).to(torch.int8)
+            w = torch.randint(-128, 128, (N, stride), device=DEV, dtype=torch.int32).to(torch.int8)
+            xs, ws = torch.rand(M, device=DEV), torch.rand(N, device=DEV)
+            out = torch.full((M + 1, os), 7.0, device=DEV)
+            for _ in range(2):
+                api.matmul_int8(api.int8_problem(M, K, N, True, x_stride=stride, w_stride=stride, out_stride=os), x, xs,
+                                w, ws, out, status)
+            want = (x[:, :K].double() @ w[:, :K].double().t()).float() * xs[:, None] * ws[None, :]
+            assert torch.equal(out[:M, :N], want), (M, N, K)
+            assert (out[M] == 7).all() and (out[:M, N:] == 7).all(), (M, N, K, os)
+    assert int(status.item()) == api.MOE_OK
 
 
 def test_router_logits_same_bits_every_time():
