@@ -160,8 +160,8 @@ int dense_stage_blocks(int kind, int rows, int nt, int splits, int64_t ctas, int
 // each its share of the k blocks at the slowest of issue, loads and MMAs,
 // plus what a tile costs besides.  The constants are a fit to timings of 32
 // sizes, from 1 x 60 x 2048 to 16384 x 128 x 8192 bytes, at every width and
-// split; of 28 sizes timed again it takes the fastest or one within 5 % for 23,
-// within 15 % for the others.
+// split; of 28 sizes timed again (these and the CTA pairs) the choice is the
+// fastest or within 5 % of it for 22, and within 15 % for the others.
 template <int KIND>
 DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
   constexpr int kWidest = KIND == KIND_I8 ? 256 : 128;

@@ -124,3 +124,31 @@ def test_norm_codes_through_the_integer_product(M, H, N):
     bound = step * np.abs(wq.double().cpu().numpy() * ws.double().cpu().numpy()[:, None]).sum(axis=1)[None, :]
     assert (np.abs(out.double().cpu().numpy() - real) <= bound * (1 + 2.0 ** -10) + 2.0 ** -16 * np.abs(y).sum(
         axis=1)[:, None] * 127 * ws.double().cpu().numpy()[None, :]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+def test_a_block_beside_integer_products_on_another_stream(fmt):
+    """The routed layer's kernels hold all tensor memory of an SM; the products
+    on the other stream take what is free and neither waits for the other for good."""
+    p = _problem(fmt, M=24)
+    host, d, L, x, r, w, router, scale = _block(p, seed=8)
+    want, want_res = L.forward_prenorm(x, w, router, residual=r, bias=d["bias"])
+    dev = device()
+    g = torch.Generator().manual_seed(9)
+    wq = torch.randint(-127, 128, (700, 1024), generator=g, dtype=torch.int32).to(torch.int8)
+    xq = torch.randint(-127, 128, (900, 1024), generator=g, dtype=torch.int32).to(torch.int8)
+    lin = layer.Int8Linear(wq.to(dev), torch.ones(700, device=dev))
+    gx, xs = xq.to(dev), torch.ones(900, device=dev)
+    a, b = torch.cuda.Stream(dev), torch.cuda.Stream(dev)
+    torch.cuda.synchronize()
+    for i in range(20):
+        out, res = L.forward_prenorm(x, w, router, residual=r, bias=d["bias"], stream=a)
+        prod = lin.forward(gx[:900 - 40 * i], xs[:900 - 40 * i], out_dtype=torch.float32, stream=b)
+    torch.cuda.synchronize()
+    L.check_status()
+    lin.check_status()
+    y = bf16_to_np(want)
+    assert torch.equal(res, want_res)
+    # FP32 rows added in any order: 2^-20 of the sum of 3 terms, then one BF16 step
+    assert (np.abs(bf16_to_np(out) - y) <= 2.0 ** -20 * np.abs(y).max() + 2 * bf16_half_ulp(y)).all()
+    assert np.array_equal(prod.cpu().numpy(), B.int8_sums(xq[:140].numpy(), wq.numpy()).astype(np.float32))
