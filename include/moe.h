@@ -427,9 +427,9 @@ typedef struct {
  * with the same stride), weight [H].  Per token, in FP32:
  *   h = x + residual_in,  residual_out = round(h),
  *   y = (h * rstd) * weight,  rstd = 1 / sqrt(sum(h^2) / H + eps)
- * (the unrounded h is normalised; the sum is held in FP64 and the products
- * carry their rounding errors along, so y is within about one FP32 rounding),
- * and y, rounded once,
+ * (the unrounded h is normalised; warps' sums are added in FP64 and the codes'
+ * products carry their rounding errors along; y / s takes s before its own
+ * rounding), and y, rounded once,
  *   to BF16 in norm_out [M, H] (may be NULL unless the format is BF16), and
  *   to codes [M, H] with scales as the format says:
  *     FP8_E4M3_B128    per 128 columns s = amax / 448, q = e4m3(y / s);

@@ -95,20 +95,32 @@ __device__ __forceinline__ float divided(float a) {
   return fmaf(fmaf(-d, q, a), z, q);
 }
 
-// Scale amax / kTop and its reciprocal.  A maximum that is not finite gives
-// NaN for both (every code of the block becomes NaN, an 8-bit integer 0); a
-// quotient below the smallest normal FP32 number, whose reciprocal may not
-// exist, gives 0 for both.
+// The bits of (a maximum of |h w|, as bits) * r; NaN stays NaN.
+__device__ __forceinline__ uint32_t amax_of(uint32_t m, const Two& r) {
+  const float p = __uint_as_float(m);
+  return abs_bits(fmaf(p, r.hi, __fmul_rn(p, r.lo)));
+}
+
+// Scale amax / kTop of values y = h w r whose largest |h w| has the bits m, and
+// the factor f of h w that makes their codes: kTop / max |h w|, which is y / s
+// before the rounding of s.  A maximum that is not finite gives NaN for both
+// (every code of the block becomes NaN, an 8-bit integer 0); a scale below the
+// smallest normal FP32 number gives 0 for both.
 template <int kTop>
-__device__ __forceinline__ float scale_of(uint32_t amax_bits, Two& inv) {
-  const float s = divided<kTop>(__uint_as_float(amax_bits));
-  inv = reciprocal(s);
-  if (amax_bits >= kInfBits) {
-    inv = {__uint_as_float(0x7FC00000u), 0.0f};
-    return inv.hi;
+__device__ __forceinline__ float scale_of(uint32_t m, const Two& r, Two& f) {
+  const uint32_t amax = amax_of(m, r);
+  const float s = divided<kTop>(__uint_as_float(amax));
+  const float p = __uint_as_float(m);
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(p));
+  f.hi = __fmul_rn(static_cast<float>(kTop), inv);
+  f.lo = __fmul_rn(inv, fmaf(-p, f.hi, static_cast<float>(kTop)));
+  if (amax >= kInfBits) {
+    f = {__uint_as_float(0x7FC00000u), 0.0f};
+    return f.hi;
   }
   if (abs_bits(s) < kMinNormalBits) {
-    inv = {0.0f, 0.0f};
+    f = {0.0f, 0.0f};
     return 0.0f;
   }
   return s;
@@ -125,12 +137,6 @@ __device__ __forceinline__ float product3(float h, float w, const Two& f) {
   const float p = __fmul_rn(h, w);
   const float e = fmaf(h, w, -p);
   return fmaf(p, f.hi, fmaf(p, f.lo, __fmul_rn(e, f.hi)));
-}
-
-// The bits of (a maximum of |h w|, as bits) * r; NaN stays NaN.
-__device__ __forceinline__ uint32_t amax_of(uint32_t m, const Two& r) {
-  const float p = __uint_as_float(m);
-  return abs_bits(fmaf(p, r.hi, __fmul_rn(p, r.lo)));
 }
 
 // max(m, |v|); NaN if either is.
@@ -282,9 +288,8 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, float (
       } else if (FMT == NQ_FP8) {
 #pragma unroll
         for (int off = 8; off; off >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-        Two inv;
-        const float s = scale_of<448>(amax_of(m, r), inv);
-        const Two f = product(r, inv);
+        Two f;
+        const float s = scale_of<448>(m, r, f);
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = product3(h[i][j], w[j], f);
@@ -317,9 +322,8 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, float (
     if (lane == 0) sh.top[warp] = row_max;
     __syncthreads();
     row_max = __reduce_max_sync(0xFFFFFFFFu, lane < nwarps ? sh.top[lane] : 0u);
-    Two inv;
-    const float s = scale_of<127>(amax_of(row_max, r), inv);
-    const Two f = product(r, inv);
+    Two f;
+    const float s = scale_of<127>(row_max, r, f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = i * blockDim.x + threadIdx.x;

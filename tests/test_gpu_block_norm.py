@@ -7,7 +7,8 @@ FP64 from there, so the mean is within 14 u, and the square root halves that:
 rstd within 7 u.  y, for a scale or BF16: 7 + 1 for h, and at most 3 for
 rstd's first part and two products: 11 u; a scale, the quotient of a maximum:
 12 u.  A code's value: 8 u, its products' errors carried along (terms of order
-u^2), and 1 for the rounding of the result.  All within 16 u = 2^-20, relative,
+u^2), 1 for the rounding of the result, and 2 between a block's scale and the
+quotient that it is the rounding of.  All within 16 u = 2^-20, relative,
 element by element.  What is rounded to
 fewer bits must lie between the roundings of v (1 - 2^-20) and v (1 + 2^-20)
 (rounding is monotonic); a code, of y / s with s the scale that the kernel
