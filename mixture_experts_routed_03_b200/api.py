@@ -126,6 +126,26 @@ class WorkspaceOffsets(ctypes.Structure):
 
 
 _lib = None
+_call = None      # the extension's call(address, *args)
+_address = {}     # entry point -> address, for it
+
+
+def _short(name):
+    """(call, address) of an entry point that is called through the extension
+    of csrc/binding.c: ctypes marshals ten arguments in two microseconds, as
+    long as the kernels of a few tokens take."""
+    global _call
+    if _call is None:
+        L = lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the _binding extension is missing: run __graft_entry__.build() "
+                               "(or python -m mixture_experts_routed_03_b200.build)") from e
+        for n in ("moe_rmsnorm_quantize", "moe_router_logits", "moe_matmul_int8"):
+            _address[n] = ctypes.cast(getattr(L, n), ctypes.c_void_p).value
+        _call = _binding.call
+    return _call, _address[name]
 
 
 def lib():
@@ -196,6 +216,11 @@ def _stream(s):
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _expect_struct(prob, cls):
+    if type(prob) is not cls:
+        raise TypeError(f"expected a {cls.__name__}, got {type(prob).__name__}")
 
 
 def _check(fn, code):
@@ -334,8 +359,10 @@ def rmsnorm_quantize(prob, x, weight, residual_in=None, residual_out=None, norm_
                      static_scale=None, stream=None):
     """Residual addition, RMS norm and activation encoding in one pass (see
     include/moe.h); prob: a NormProblem."""
-    code = lib().moe_rmsnorm_quantize(prob, _ptr(x), _ptr(residual_in), _ptr(weight), _ptr(static_scale),
-                                      _ptr(residual_out), _ptr(norm_out), _ptr(codes), _ptr(scales), _stream(stream))
+    _expect_struct(prob, NormProblem)
+    call, at = _short("moe_rmsnorm_quantize")
+    code = call(at, ctypes.addressof(prob), x, residual_in, weight, static_scale, residual_out, norm_out, codes, scales,
+                _stream(stream))
     if code:
         raise MoEError("moe_rmsnorm_quantize", code)
 
@@ -343,8 +370,9 @@ def rmsnorm_quantize(prob, x, weight, residual_in=None, residual_out=None, norm_
 def router_logits(prob, x_bf16, router_weight, logits, device_status, stream=None):
     """Router logits fp32 [M, E] of BF16 rows (see include/moe.h); prob: the
     layer's Problem, device_status: an int32 on the device (or a workspace)."""
-    code = lib().moe_router_logits(prob, _ptr(x_bf16), _ptr(router_weight), _ptr(logits), _ptr(device_status),
-                                   _stream(stream))
+    _expect_struct(prob, Problem)
+    call, at = _short("moe_router_logits")
+    code = call(at, ctypes.addressof(prob), x_bf16, router_weight, logits, device_status, _stream(stream))
     if code:
         raise MoEError("moe_router_logits", code)
 
@@ -352,8 +380,9 @@ def router_logits(prob, x_bf16, router_weight, logits, device_status, stream=Non
 def matmul_int8(prob, x, x_scale, w, w_scale, out, device_status, bias=None, stream=None):
     """Product of 8-bit integers with a scale per token and per channel (see
     include/moe.h); prob: an Int8Problem."""
-    code = lib().moe_matmul_int8(prob, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(out),
-                                 _ptr(device_status), _stream(stream))
+    _expect_struct(prob, Int8Problem)
+    call, at = _short("moe_matmul_int8")
+    code = call(at, ctypes.addressof(prob), x, x_scale, w, w_scale, bias, out, device_status, _stream(stream))
     if code:
         raise MoEError("moe_matmul_int8", code)
 

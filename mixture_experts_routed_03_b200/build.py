@@ -6,13 +6,16 @@ The library is two translation units (``csrc/moe_api.cu``, the routed layer, and
 ``csrc/block_api.cu``, the operators next to it), each including its kernel
 headers and compiled to an object of its own, side by side; the runtime is
 linked statically and the driver's tensor-map encoder is looked up at run
-time, so the .so needs no libcuda at link time.
+time, so the .so needs no libcuda at link time.  ``_binding.so`` is the
+Python extension of ``csrc/binding.c``.
 """
 
 import os
 import re
+import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +26,9 @@ SOURCES = ["moe_api.cu", "block_api.cu"]
 # the tensor-core peak probe the benchmark reports its roofline against
 PEAK_OUT = os.path.join(HERE, "libmoe_peak.so")
 PEAK_SOURCES = ["mma_peak.cu"]
+# the Python extension that makes the short calls (csrc/binding.c)
+BINDING_OUT = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = "binding.c"
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -92,6 +98,12 @@ def build(force=False, verbose=False):
             log = _compile(out, sources, log_name, force)
             if verbose:
                 print(log)
+    if force or not up_to_date(BINDING_OUT, [BINDING_SOURCE]):
+        cc = shutil.which("gcc") or shutil.which("cc") or "cc"
+        rc, log = _run([cc, "-O2", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"], "-o", BINDING_OUT,
+                        os.path.join(CSRC, BINDING_SOURCE)])
+        if rc != 0:
+            raise RuntimeError("cc failed:\n" + log[-4000:])
     return OUT
 
 

@@ -199,3 +199,40 @@ def test_int8_linear_pads_odd_rows_once():
     assert torch.equal(lin.weight, w)
     kept = torch.zeros((4, 32), dtype=torch.int8)
     assert layer.Int8Linear(kept, torch.ones(4)).weight.data_ptr() == kept.data_ptr()
+
+
+# ------------------------------------------------------------------ the binding of the short calls
+
+def test_binding_takes_tensors_integers_and_none(lib):
+    x = torch.zeros(16)
+    api.rmsnorm_quantize(api.norm_problem(0, 256, "int8"), None, x, codes=_at(0), stream=0)
+    api.router_logits(api.problem(0, 256, 128, 8, 2), x, None, _at(0), x, stream=0)
+    api.matmul_int8(api.int8_problem(0, 64, 8), x, x, None, _at(1), x, x, stream=0)
+
+
+def test_binding_raises_the_librarys_errors(lib):
+    for call in (lambda: api.rmsnorm_quantize(api.norm_problem(4, 100, "fp8"), None, None, stream=0),
+                 lambda: api.router_logits(api.problem(4, 256, 128, 8, 2), _at(0, 8), _at(1), _at(2), _at(3), stream=0),
+                 lambda: api.matmul_int8(api.int8_problem(4, 64, 8), _at(0), _at(1), _at(2), _at(3), _at(5, 1), _at(6),
+                                         stream=0)):
+        with pytest.raises(api.MoEError) as e:
+            call()
+        assert e.value.code == BAD and "MOE_ERR_INVALID_ARG" in str(e.value)
+
+
+def test_binding_refuses_what_is_no_problem_or_pointer(lib):
+    with pytest.raises(TypeError):
+        api.rmsnorm_quantize(api.int8_problem(4, 64, 8), None, None, stream=0)
+    with pytest.raises(TypeError):
+        api.matmul_int8(api.norm_problem(4, 256), None, None, None, None, None, None, stream=0)
+    with pytest.raises(TypeError):
+        api.router_logits(None, None, None, None, None, stream=0)
+    with pytest.raises(AttributeError):
+        api.router_logits(api.problem(4, 256, 128, 8, 2), "x", None, None, None, stream=0)
+
+
+def test_binding_function_checks_its_own_arguments(lib):
+    call, at = api._short("moe_router_logits")
+    for args in ((), (at,), (at, 0), (at,) + (0,) * 13):
+        with pytest.raises(TypeError):
+            call(*args)
