@@ -8,6 +8,7 @@
 #include "dense.cuh"
 #include "dense_few.cuh"
 #include "dense_pair.cuh"
+#include "dense_warps.cuh"
 #include "host.cuh"
 #include "norm.cuh"
 
@@ -256,6 +257,44 @@ cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap&
   return cudaLaunchKernelEx(&cfg, dense_kernel<KIND, NT>, p, tx, tw);
 }
 
+struct WarpsPlan {
+  int xt, splits;
+  double cost;      // estimated ns
+};
+
+// Tile and K split of dense_warps_kernel by estimated time: launch and join,
+// the rounds of loads, the CTAs on an SM, the bytes from HBM and those from L2.
+// A fit (9 % rms) to timings of 204 sizes from 4 x 128 x 256 to 2048 x 256 x
+// 16384 at every split; by it, and plan_dense's estimate where that is less, the
+// choice takes 2 % longer than the best one on average, 19 % at most.
+WarpsPlan plan_warps(int64_t M, int N, int64_t k_bytes, int sms) {
+  WarpsPlan best{1, 1, 1e300};
+  const int groups = static_cast<int>(k_bytes / kWarpsGroup);
+  for (int xt = 1; xt <= 4; xt += 3) {
+    const int64_t tiles = (M + 8 * xt - 1) / (8 * xt) * ((N + 15) / 16);
+    for (int s = 1; s <= 8; s *= 2) {
+      if ((s > 1 && groups < 4 * s) || tiles * s > int64_t(16) * sms) break;
+      const double ctas = static_cast<double>(tiles * s);
+      const int64_t slots = int64_t(cluster_slots(s, sms)) * warps_blocks(xt);
+      const double waves = static_cast<double>((tiles * s + slots - 1) / slots);
+      const double per_sm = static_cast<double>((tiles * s + sms - 1) / sms);
+      const double rounds = ((groups + s - 1) / s + kFewWarps - 1) / kFewWarps;
+      const double cost = 1690.0 + (s > 1 ? 870.0 : 0.0) + rounds * (132.0 * per_sm + 53.0 * waves * (xt + 2)) +
+                          171.0 * waves + 0.76 * ctas + 120.0 * per_sm * xt +
+                          static_cast<double>(k_bytes) * (22e-6 * (M + N) + 22.4e-6 * (16 + 8 * xt) * tiles);
+      if (cost < best.cost) best = {xt, s, cost};
+    }
+  }
+  return best;
+}
+
+template <int XT, int S>
+cudaError_t launch_warps(const FewArgs& a, cudaStream_t st) {
+  const int n_tiles = (a.N + 15) / 16;
+  return launch_k(dense_warps_kernel<XT, S>, (a.M + 8 * XT - 1) / (8 * XT) * n_tiles * S, kFewWarps * 32, 0, st, a,
+                  n_tiles);
+}
+
 template <int KIND, int MB, int R, int D>
 cudaError_t launch_few(const FewArgs& a, int sms, cudaStream_t st) {
   // warps that share a row: as many as it takes to give every SM two blocks,
@@ -273,9 +312,8 @@ cudaError_t launch_few(const FewArgs& a, int sms, cudaStream_t st) {
   }
 }
 
-template <int KIND>
-moe_status_t run_few(const DenseArgs& p, const void* x, const void* w, int64_t k_bytes, int64_t x_stride,
-                     int64_t w_stride, int sms, cudaStream_t st) {
+FewArgs few_args(const DenseArgs& p, const void* x, const void* w, int64_t k_bytes, int64_t x_stride,
+                 int64_t w_stride) {
   FewArgs a{};
   a.x = static_cast<const uint8_t*>(x);
   a.w = static_cast<const uint8_t*>(w);
@@ -290,11 +328,30 @@ moe_status_t run_few(const DenseArgs& p, const void* x, const void* w, int64_t k
   a.bias = p.bias;
   a.out = p.out;
   a.out_stride = p.out_stride;
+  return a;
+}
+
+template <int KIND>
+moe_status_t run_few(const FewArgs& a, int sms, cudaStream_t st) {
   cudaError_t e;
   if (a.M == 1) e = launch_few<KIND, 1, 2, 4>(a, sms, st);
   else if (a.M == 2 || KIND == KIND_I8) e = launch_few<KIND, 2, 2, 4>(a, sms, st);
-  else if (a.M <= 4) e = launch_few<KIND_BF16, 4, 2, 4>(a, sms, st);
-  else e = launch_few<KIND_BF16, 8, 2, 2>(a, sms, st);
+  else e = launch_few<KIND_BF16, 4, 2, 4>(a, sms, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t run_warps(const WarpsPlan& pl, const FewArgs& a, cudaStream_t st) {
+  cudaError_t e;
+  switch (pl.xt * 10 + pl.splits) {
+    case 11: e = launch_warps<1, 1>(a, st); break;
+    case 12: e = launch_warps<1, 2>(a, st); break;
+    case 14: e = launch_warps<1, 4>(a, st); break;
+    case 18: e = launch_warps<1, 8>(a, st); break;
+    case 41: e = launch_warps<4, 1>(a, st); break;
+    case 42: e = launch_warps<4, 2>(a, st); break;
+    case 44: e = launch_warps<4, 4>(a, st); break;
+    default: e = launch_warps<4, 8>(a, st); break;
+  }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -344,12 +401,15 @@ template <int KIND>
 moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_bytes, int64_t x_stride, int64_t w_stride,
                        cudaStream_t st) {
   const int sms = sm_count();
-  if (p.M <= kFewMaxM<KIND>) return run_few<KIND>(p, x, w, k_bytes, x_stride, w_stride, sms, st);
+  if (p.M <= kFewMaxM<KIND>) return run_few<KIND>(few_args(p, x, w, k_bytes, x_stride, w_stride), sms, st);
   p.k_blocks = static_cast<int>((k_bytes + 127) / 128);
   const DensePlan pl = plan_dense<KIND>(p.M, p.N, p.k_blocks, sms);
   if (KIND == KIND_I8) {
     const DensePlan pp = plan_pair(p.M, p.N, p.k_blocks, sms);
     if (pp.cost < pl.cost) return run_pair(p, pp.nt, x, w, k_bytes, x_stride, w_stride, sms, st);
+  } else {
+    const WarpsPlan pw = plan_warps(p.M, p.N, k_bytes, sms);
+    if (pw.cost < pl.cost) return run_warps(pw, few_args(p, x, w, k_bytes, x_stride, w_stride), st);
   }
   p.splits = pl.splits;
   p.tile_rows = pl.tile_rows;

@@ -13,7 +13,8 @@
 // clusters).  Integers, 1 x 4096 x 7168, w from HBM: 6.6 us (4.5 TB/s, launch
 // included) against 9.4; the integer dot products bound it from 3 rows on
 // (12.5 us at 4 rows, tiles 9.4), so it takes 1 or 2.  BF16, 256 x 7168 in L2:
-// 2.2 us at 1 row and 3.6 at 8, tiles 6.9 and 7.2; it takes up to 8.
+// 2.2 us at 1 row and 2.8 at 4, the MMAs of dense_warps.cuh 3.2 and 3.1; it
+// takes up to 4 (at 8 rows 3.7 against 3.3).
 #pragma once
 
 #include "dense.cuh"
@@ -22,7 +23,7 @@ namespace moe {
 
 constexpr int kFewWarps = 8;
 template <int KIND>
-constexpr int kFewMaxM = KIND == KIND_I8 ? 2 : 8;
+constexpr int kFewMaxM = KIND == KIND_I8 ? 2 : 4;
 
 struct FewArgs {
   const uint8_t* x;
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) dense_few_kernel(const __grid_
   for (int c = slice * 32 + lane; c < chunks; c += kDepth * kStep) {
     // A row's last group of loads is filled up with zeros, so that all its loads
     // are in flight at once; one by one they cost 0.55 us at 1 x 4096 x 7168
-    // (7.1 -> 6.6 us) and at 8 x 256 x 7168 in BF16 (4.2 -> 3.6).
+    // (7.1 -> 6.6 us).
     uint4 wv[R][kDepth];
 #pragma unroll
     for (int d = 0; d < kDepth; ++d)

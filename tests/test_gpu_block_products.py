@@ -187,6 +187,59 @@ def test_router_logits(M, E, H):
     assert (buf[M] == 3).all() and int(status.item()) == api.MOE_OK
 
 
+@pytest.mark.parametrize("M,E,H", [(5, 1, 256), (48, 65, 512), (33, 1, 2816), (130, 60, 5120), (7, 1023, 5120),
+                                   (16, 250, 2816), (24, 161, 4096), (5, 1, 8192), (9, 257, 7168), (777, 61, 256),
+                                   (49, 1024, 1024), (31, 1023, 2816), (129, 250, 5120), (64, 256, 7168), (33, 513, 8192),
+                                   (97, 160, 7168), (63, 64, 16384), (6, 7, 768), (65, 9, 1280)])
+def test_router_logits_of_a_batch(M, E, H):
+    """The warps' MMAs at every split of K and height of tile, rows and experts that do not fill one."""
+    x, w = _router(M, E, H, seed=M + E)
+    buf = torch.full((M + 1, E), 3.0, device=DEV)
+    status = _status()
+    api.router_logits(api.problem(M, H, 128, E, 1), x.to(DEV), w.to(DEV), buf, status)
+    _check_logits(buf[:M], x, w)
+    assert (buf[M] == 3).all() and int(status.item()) == api.MOE_OK
+
+
+@pytest.mark.parametrize("M,E,H", [(9, 40, 256), (64, 256, 7168), (40, 17, 4096)])
+def test_router_values_that_are_not_finite_stay_in_their_row_and_column(M, E, H):
+    """The last row and the last expert stand in for those past the ends: what they hold must not spread."""
+    x, w = _router(M, E, H, seed=31)
+    x[M - 1, H - 1], w[E - 1, 0], x[2, 5] = float("nan"), float("inf"), float("inf")
+    out = torch.empty((M, E), device=DEV)
+    api.router_logits(api.problem(M, H, 128, E, 1), x.to(DEV), w.to(DEV), out, _status())
+    assert torch.isnan(out[M - 1]).all() and not torch.isfinite(out[2]).any() and not torch.isfinite(out[:, E - 1]).any()
+    keep = [i for i in range(M - 1) if i != 2]
+    _check_logits(out[keep][:, :E - 1], x[keep], w[:E - 1])
+
+
+def test_router_batches_in_a_graph_beside_calls_on_another_stream():
+    cases = [(_router(M, 256, 7168, seed=M), M) for M in (9, 64)]
+    cases = [(x.to(DEV), w.to(DEV), torch.empty((M, 256), device=DEV), M) for (x, w), M in cases]
+    status = _status()
+
+    def run(case):
+        x, w, out, M = case
+        api.router_logits(api.problem(M, 7168, 128, 256, 1), x, w, out, status)
+
+    for c in cases:
+        run(c)
+    want = [c[2].clone() for c in cases]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        for _ in range(5):
+            run(cases[0])
+    for c in cases:
+        c[2].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        graph.replay()
+        with torch.cuda.stream(side):
+            run(cases[1])
+    torch.cuda.synchronize()
+    assert torch.equal(cases[0][2], want[0]) and torch.equal(cases[1][2], want[1])
+
+
 def test_products_of_many_shapes_one_after_the_other():
     """Calls of changing shapes back to back, two of each: nothing of one may reach the next."""
     import math
