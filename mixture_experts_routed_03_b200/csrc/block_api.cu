@@ -265,8 +265,9 @@ struct WarpsPlan {
 // Tile and K split of dense_warps_kernel by estimated time: launch and join,
 // the rounds of loads, the CTAs on an SM, the bytes from HBM and those from L2.
 // A fit (9 % rms) to timings of 204 sizes from 4 x 128 x 256 to 2048 x 256 x
-// 16384 at every split; by it, and plan_dense's estimate where that is less, the
-// choice takes 2 % longer than the best one on average, 19 % at most.
+// 16384 at every split, and 650 ns, by which plan_dense's estimates of small
+// calls are longer than their kernels; by the lesser of the two the choice
+// takes 2.5 % longer than the best one on average, 19 % at most.
 WarpsPlan plan_warps(int64_t M, int N, int64_t k_bytes, int sms) {
   WarpsPlan best{1, 1, 1e300};
   const int groups = static_cast<int>(k_bytes / kWarpsGroup);
@@ -274,14 +275,13 @@ WarpsPlan plan_warps(int64_t M, int N, int64_t k_bytes, int sms) {
     const int64_t tiles = (M + 8 * xt - 1) / (8 * xt) * ((N + 15) / 16);
     for (int s = 1; s <= 8; s *= 2) {
       if ((s > 1 && groups < 4 * s) || tiles * s > int64_t(16) * sms) break;
-      const double ctas = static_cast<double>(tiles * s);
       const int64_t slots = int64_t(cluster_slots(s, sms)) * warps_blocks(xt);
       const double waves = static_cast<double>((tiles * s + slots - 1) / slots);
       const double per_sm = static_cast<double>((tiles * s + sms - 1) / sms);
       const double rounds = ((groups + s - 1) / s + kFewWarps - 1) / kFewWarps;
-      const double cost = 1690.0 + (s > 1 ? 870.0 : 0.0) + rounds * (132.0 * per_sm + 53.0 * waves * (xt + 2)) +
-                          171.0 * waves + 0.76 * ctas + 120.0 * per_sm * xt +
-                          static_cast<double>(k_bytes) * (22e-6 * (M + N) + 22.4e-6 * (16 + 8 * xt) * tiles);
+      const double cost = 1380.0 + (s > 1 ? 886.0 : 0.0) + rounds * (133.0 * per_sm + 52.0 * waves * (xt + 2)) +
+                          363.0 * waves + 119.0 * per_sm * xt +
+                          static_cast<double>(k_bytes) * (30e-6 * (M + N) + 22e-6 * (16 + 8 * xt) * tiles);
       if (cost < best.cost) best = {xt, s, cost};
     }
   }

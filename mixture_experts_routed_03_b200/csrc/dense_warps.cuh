@@ -12,8 +12,8 @@
 // What bounds it: up to some hundred rows latency, then that w is read again
 // for every 8 XT rows of x and x for every 16 of w, which grows with M N; there
 // the tcgen05 tiles of dense.cuh are faster.  H = 7168, 256 experts, against
-// those: 9 rows 3.5 us (tiles 6.8), 64 rows 5.1 (7.7), 128 rows 6.3 (7.8), 256
-// rows 8.6 (10.3), 777 rows 26 (11.8); 64 x 60 x 2048: 2.6 (5.0).  XT is 1 or 4:
+// those: 9 rows 3.4 us (tiles 6.8), 64 rows 5.1 (7.7), 128 rows 6.3 (7.8), 256
+// rows 8.3 (10.4), 777 rows 26 (11.8); 64 x 60 x 2048: 2.4 (5.0).  XT is 1 or 4:
 // with 2 between them the best choice was 1 % faster on average.  Integers by
 // the same instructions' 8-bit forms were slower than the tiles from 16 rows on
 // (64 x 4096 x 7168: 21 us against 9.6) and hardly faster below.
@@ -79,10 +79,9 @@ __global__ void __cluster_dims__(S, 1, 1) __launch_bounds__(kFewWarps * 32, warp
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[j][q] = sum[j][q] = 0.0f;
 
-  int chain = 0;
-  for (int c = from + warp; c < to; c += kFewWarps) {
+  uint4 wv[2][2], xv[2][XT];
+  auto fetch = [&](int c) {
     const int base = c * kWarpsGroup + t * 16;
-    uint4 wv[2][2], xv[2][XT];
 #pragma unroll
     for (int d = 0; d < 2; ++d) {
 #pragma unroll
@@ -90,6 +89,12 @@ __global__ void __cluster_dims__(S, 1, 1) __launch_bounds__(kFewWarps * 32, warp
 #pragma unroll
       for (int i = 0; i < XT; ++i) xv[d][i] = *reinterpret_cast<const uint4*>(xr[i] + base + d * 64);
     }
+  };
+  // The next group is asked for once the MMAs have read this one; two or three
+  // groups ahead, for which an SM then holds fewer blocks, measured the same.
+  int c = from + warp, chain = 0;
+  if (c < to) fetch(c);
+  for (; c < to; c += kFewWarps) {
 #pragma unroll
     for (int d = 0; d < 2; ++d)
 #pragma unroll
@@ -98,6 +103,7 @@ __global__ void __cluster_dims__(S, 1, 1) __launch_bounds__(kFewWarps * 32, warp
         mma_warp(acc[j], a.x, b.x, a.y, b.y, x.x, x.y);
         mma_warp(acc[j], a.z, b.z, a.w, b.w, x.z, x.w);
       }
+    if (c + kFewWarps < to) fetch(c + kFewWarps);
     if (++chain == 4) {
       chain = 0;
 #pragma unroll

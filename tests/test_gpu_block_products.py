@@ -190,7 +190,8 @@ def test_router_logits(M, E, H):
 @pytest.mark.parametrize("M,E,H", [(5, 1, 256), (48, 65, 512), (33, 1, 2816), (130, 60, 5120), (7, 1023, 5120),
                                    (16, 250, 2816), (24, 161, 4096), (5, 1, 8192), (9, 257, 7168), (777, 61, 256),
                                    (49, 1024, 1024), (31, 1023, 2816), (129, 250, 5120), (64, 256, 7168), (33, 513, 8192),
-                                   (97, 160, 7168), (63, 64, 16384), (6, 7, 768), (65, 9, 1280)])
+                                   (97, 160, 7168), (63, 64, 16384), (6, 7, 768), (65, 9, 1280), (9, 1023, 7168),
+                                   (31, 250, 8192)])
 def test_router_logits_of_a_batch(M, E, H):
     """The warps' MMAs at every split of K and height of tile, rows and experts that do not fill one."""
     x, w = _router(M, E, H, seed=M + E)
