@@ -54,8 +54,18 @@ moe_status_t check_norm(const moe_norm_t* n) {
   return MOE_OK;
 }
 
+// While a block works on its row it has no loads in flight, so each asks L2 for
+// the row that a later block will read, some 3 MB further on (2 to 5 measured
+// alike; a whole wave of blocks, 10 MB and more, was slower than none): 4096 x
+// 7168 FP8 53.5 -> 45.7 us, 8192 x 16384 288 -> 213, 16384 x 4096 MXFP8 116 ->
+// 101.  Below 48 MB of inputs it gains nothing.
+constexpr int64_t kNormAhead = 3 << 20, kNormAheadFrom = 48 << 20;
+
 template <int FMT, int RES, int NV, int kThreads, int kBlocks>
-cudaError_t launch_norm_rows(const NormArgs& a, int64_t M, int threads, cudaStream_t st) {
+cudaError_t launch_norm_rows(NormArgs a, int64_t M, int threads, cudaStream_t st) {
+  const int64_t row_bytes = int64_t(a.H) * (RES == NR_NONE ? 2 : RES == NR_BF16 ? 4 : 6);
+  a.M = M;
+  a.ahead = M * row_bytes >= kNormAheadFrom ? kNormAhead / row_bytes : 0;
   return launch_k(rmsnorm_quantize_kernel<FMT, RES, NV, kThreads, kBlocks>, static_cast<int>(M), threads, 0, st, a);
 }
 
@@ -66,7 +76,8 @@ cudaError_t launch_norm_rows(const NormArgs& a, int64_t M, int threads, cudaStre
 //     4096: 3.5 us against 4.7);
 //   else two, which halves the threads that share a row's reductions, five
 //     blocks an SM (4096 x 2048: 11.8 us against 12.4; 16384 x 4096, FP32
-//     residual: 139 against 146), while a block can hold the row;
+//     residual: 139 against 146, both without the requests to L2), while a
+//     block can hold the row;
 //   above 16384 columns four.
 template <int FMT, int RES>
 cudaError_t launch_norm(const NormArgs& a, int64_t M, cudaStream_t st) {

@@ -14,7 +14,13 @@
 // stores, so each byte crosses once.  A block serves a row at a time, every
 // thread holding NV vectors of 8 consecutive columns, vector v = i * threads +
 // tid, so that 16 (4) neighbouring lanes hold one 128- (32-) column block and
-// its maximum is a few shuffles.
+// its maximum is a few shuffles.  What keeps it from the copy rate is a block's
+// pause between its loads and its stores, in which it asks for nothing, and the
+// 30 (8-bit codes) or 19 (BF16) instructions an element.  Against the first, a
+// block asks L2 for the row that a later one will read; against the second, two
+// columns go through one instruction (f32x2) where FP32 allows it, 39 -> 33.
+// 16384 x 4096, FP32 residual, FP8: 131 us of 135 at the copy rate (some of it
+// is still in L2); 4096 x 7168, BF16 residual, FP8: 46 of 41.
 //
 // Roundings.  A code changes where its value crosses the midpoint of two, so
 // the value is kept to about one FP32 rounding: the warps' FP32 sums of
@@ -46,6 +52,8 @@ struct NormArgs {
   int weight_fp32;
   float eps;
   double inv_H;            // 1 / H
+  int64_t M;
+  int64_t ahead;           // the row that a block asks L2 for is this many further on; 0: none
 };
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4& u, float (&v)[8]) {
@@ -132,11 +140,62 @@ __device__ __forceinline__ Two product(const Two& a, const Two& b) {
   return {hi, fmaf(a.lo, b.hi, fmaf(a.hi, b.lo, fmaf(a.hi, b.hi, -hi)))};
 }
 
-// h * w * f, rounded once.
-__device__ __forceinline__ float product3(float h, float w, const Two& f) {
-  const float p = __fmul_rn(h, w);
-  const float e = fmaf(h, w, -p);
-  return fmaf(p, f.hi, fmaf(p, f.lo, __fmul_rn(e, f.hi)));
+// Two FP32 numbers that one instruction works on (each rounded as by itself).
+struct Pair {
+  uint64_t v;
+};
+
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
+  return p;
+}
+
+__device__ __forceinline__ void split(const Pair& p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p.v));
+}
+
+__device__ __forceinline__ Pair mul2(const Pair& a, const Pair& b) {
+  Pair p;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+
+__device__ __forceinline__ Pair add2(const Pair& a, const Pair& b) {
+  Pair p;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+
+__device__ __forceinline__ Pair fma2(const Pair& a, const Pair& b, const Pair& c) {
+  Pair p;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return p;
+}
+
+// y = h w f of 8 columns, each rounded once: p = h w carries its rounding error
+// -e = p - h w, which -h gives without a negation.
+__device__ __forceinline__ void product3(const float (&h)[8], const float (&w)[8], const Two& f, float (&y)[8]) {
+  const Pair hi = pair(f.hi, f.hi), lo = pair(f.lo, f.lo), nhi = pair(-f.hi, -f.hi);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const Pair ww = pair(w[j], w[j + 1]);
+    const Pair p = mul2(pair(h[j], h[j + 1]), ww);
+    const Pair e = fma2(pair(-h[j], -h[j + 1]), ww, p);
+    split(fma2(p, hi, fma2(p, lo, mul2(e, nhi))), y[j], y[j + 1]);
+  }
+}
+
+// y = a * b
+__device__ __forceinline__ void times8(const float (&a)[8], const float (&b)[8], float (&y)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) split(mul2(pair(a[j], a[j + 1]), pair(b[j], b[j + 1])), y[j], y[j + 1]);
+}
+
+__device__ __forceinline__ void times8(const float (&a)[8], float b, float (&y)[8]) {
+  const Pair bb = pair(b, b);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) split(mul2(pair(a[j], a[j + 1]), bb), y[j], y[j + 1]);
 }
 
 // max(m, |v|); NaN if either is.
@@ -182,6 +241,11 @@ __device__ __forceinline__ void load_weight8(const NormArgs& a, int v, float (&w
   }
 }
 
+// `bytes` (a multiple of 16) from `p` on (16-byte aligned) on their way to L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 struct NormShared {
   float sum[32];
   uint32_t top[32];
@@ -202,7 +266,10 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, float (
     if (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x) >= nvec) continue;
     float q[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = fmaf(h[i][j + 4], h[i][j + 4], __fmul_rn(h[i][j], h[i][j]));
+    for (int j = 0; j < 4; j += 2) {
+      const Pair a = pair(h[i][j], h[i][j + 1]), b = pair(h[i][j + 4], h[i][j + 5]);
+      split(fma2(b, b, mul2(a, a)), q[j], q[j + 1]);
+    }
     ss += (q[0] + q[1]) + (q[2] + q[3]);
   }
 #pragma unroll
@@ -256,32 +323,31 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, float (
     }
     float w[8];
     load_weight8(a, v, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[i][j] = __fmul_rn(h[i][j], pow2);
+    times8(h[i], pow2, h[i]);
+    float hw[8];
+    times8(h[i], w, hw);
     if (a.norm_out) {
       float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(__fmul_rn(h[i][j], w[j]), r.hi);
+      times8(hw, r.hi, y);
       *reinterpret_cast<uint4*>(normed + 8 * v) = pack_bf16x8(y);
     }
     if (FMT == NQ_FP8T) {
       const uint32_t sb = __float_as_uint(__ldg(a.static_scale));
       const bool good = sb >= kMinNormalBits && sb < kInfBits;
       const Two f = product(r, good ? reciprocal(__uint_as_float(sb)) : Two{__uint_as_float(0x7FC00000u), 0.0f});
-      float y[8];
+      float y[8], big[8];
+      product3(h[i], w, f, y);
+      times8(hw, f.hi, big);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // a product that leaves FP32's range saturates
-        const float big = __fmul_rn(__fmul_rn(h[i][j], w[j]), f.hi);
-        y[j] = abs_bits(big) == kInfBits ? big : product3(h[i][j], w[j], f);
-      }
+      for (int j = 0; j < 8; ++j)
+        if (abs_bits(big[j]) == kInfBits) y[j] = big[j];     // a product that leaves FP32's range saturates
       *reinterpret_cast<uint2*>(codes + 8 * v) = codes_e4m3(y);
     }
     if (FMT == NQ_FP8 || FMT == NQ_MXFP8 || FMT == NQ_INT8) {
       // the largest |y| is the largest |h w| times r
       float top = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max_abs(top, __fmul_rn(h[i][j], w[j]));
+      for (int j = 0; j < 8; ++j) top = max_abs(top, hw[j]);
       uint32_t m = __float_as_uint(top);       // not negative: ordered as its bits, NaN above all numbers
       if (FMT == NQ_INT8) {
         row_max = max(row_max, m);
@@ -291,8 +357,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, float (
         Two f;
         const float s = scale_of<448>(m, r, f);
         float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = product3(h[i][j], w[j], f);
+        product3(h[i], w, f, y);
         *reinterpret_cast<uint2*>(codes + 8 * v) = codes_e4m3(y);
         if ((lane & 15) == 0) static_cast<float*>(a.scales)[row * (a.H / 128) + v / 16] = s;
       } else {
@@ -309,8 +374,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, float (
         const float inv = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 - X) << 23);
         const Two f = {__fmul_rn(r.hi, inv), __fmul_rn(r.lo, inv)};
         float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = product3(h[i][j], w[j], f);
+        product3(h[i], w, f, y);
         *reinterpret_cast<uint2*>(codes + 8 * v) = codes_e4m3(y);
         if ((lane & 3) == 0)
           static_cast<uint8_t*>(a.scales)[row * (a.H / 32) + v / 4] = static_cast<uint8_t>(bad ? 255 : X + 127);
@@ -330,26 +394,28 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, float (
       if (v >= nvec) continue;
       float w[8], q[8];
       load_weight8(a, v, w);                   // again, from L1
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = product3(h[i][j], w[j], f);
+      product3(h[i], w, f, q);
       *reinterpret_cast<uint2*>(codes + 8 * v) = codes_s8(q);
     }
     if (threadIdx.x == 0) static_cast<float*>(a.scales)[row] = s;
   }
 }
 
+__device__ __forceinline__ void plus8(float (&h)[8], const float (&r)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) split(add2(pair(h[j], h[j + 1]), pair(r[j], r[j + 1])), h[j], h[j + 1]);
+}
+
 __device__ __forceinline__ void add_bf16x8(const uint4& u, float (&h)[8]) {
   float r[8];
   unpack_bf16x8(u, r);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) h[j] = __fadd_rn(h[j], r[j]);
+  plus8(h, r);
 }
 
 __device__ __forceinline__ void add_f32x8(const float4& a, const float4& b, float (&h)[8]) {
   float r[8];
   unpack_f32x8(a, b, r);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) h[j] = __fadd_rn(h[j], r[j]);
+  plus8(h, r);
 }
 
 // One block per row, of at most kThreads threads; registers for kBlocks blocks an SM.
@@ -360,6 +426,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rmsnorm_quantize_kernel(con
   pdl_wait();
   const int64_t row = blockIdx.x;
   const int nvec = a.H / 8;
+  if (a.ahead && threadIdx.x == 0 && row + a.ahead < a.M) {
+    prefetch_l2(a.x + (row + a.ahead) * a.x_stride, a.H * 2);
+    if (RES == NR_BF16)
+      prefetch_l2(static_cast<const uint16_t*>(a.res_in) + (row + a.ahead) * a.rin_stride, a.H * 2);
+    if (RES == NR_FP32) prefetch_l2(static_cast<const float*>(a.res_in) + (row + a.ahead) * a.rin_stride, a.H * 4);
+  }
   float h[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {

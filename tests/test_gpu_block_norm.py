@@ -291,6 +291,23 @@ def test_offsets_past_32_bits(fmt, H):
     assert not (out.codes[100:200].view(torch.uint8) & 0x7F).any()
 
 
+@pytest.mark.parametrize("fmt,M,H,residual", [("fp8", 1801, 7168, "bf16"), ("mxfp8", 2100, 4096, "fp32"),
+                                              ("int8", 3300, 8192, None), ("bf16", 401, 32768, "bf16"),
+                                              ("fp8_tensor", 12400, 1024, "bf16")])
+def test_many_long_rows_in_place(fmt, M, H, residual):
+    """Inputs past 48 MB, of which blocks ask L2 for the rows to come, in place and to the last row of their memory."""
+    rows = [0, 1, M // 2, M - 2, M - 1]
+    part, r, w, ss = _inputs(len(rows), H, residual, seed=23)
+    x = torch.randn((M, H), device=DEV).to(torch.bfloat16)
+    x[rows] = part
+    stream = None
+    if residual:
+        stream = torch.randn((M, H), device=DEV).to(r.dtype)
+        stream[rows] = r
+    out = layer.rmsnorm_quantize(x, w, stream, fmt, 1e-6, ss if fmt == "fp8_tensor" else None, residual_out=stream)
+    check(type(out)(*[None if t is None else t[rows] for t in out]), part, r, w, ss, fmt, 1e-6)
+
+
 def test_residual_of_the_other_rows_is_untouched_in_place():
     """In place on a slice of a longer stream: the tokens before and behind keep theirs."""
     x, r, w, ss = _inputs(40, 1024, "bf16", seed=19)
