@@ -268,23 +268,40 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
   const uint32_t block_bytes = a_bytes + NT * 128u;
   const uint32_t stage_bytes = block_bytes * p.stage_blocks;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&hdr->full[s], 1);
-      mbar_init(&hdr->empty[s], 1);
+  // The ring's first loads wait for nothing but the barriers that the loading
+  // thread sets up itself: they are under way while tensor memory is allocated.
+  auto load = [&](int stage, int kb) {
+    uint8_t* sa = ring + stage * stage_bytes;
+    const bool two = p.stage_blocks == 2 && kb + 1 < kb1;
+    mbar_arrive_expect_tx(&hdr->full[stage], two ? 2 * block_bytes : block_bytes);
+    tma_load_2d(sa + a_bytes, &tw, &hdr->full[stage], kb * 128, n0);
+    tma_load_2d(sa, &tx, &hdr->full[stage], kb * 128, static_cast<int>(m0));
+    if (two) {
+      tma_load_2d(sa + block_bytes + a_bytes, &tw, &hdr->full[stage], kb * 128 + 128, n0);
+      tma_load_2d(sa + block_bytes, &tx, &hdr->full[stage], kb * 128 + 128, static_cast<int>(m0));
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&hdr->acc_full[b], 1);
-      mbar_init(&hdr->acc_empty[b], kDenseEpiWarps);
+  };
+  if (warp == 8) {
+    if (elect_one()) {
+      prefetch_tensormap(&tx);
+      prefetch_tensormap(&tw);
+      for (int s = 0; s < p.stages; ++s) {
+        mbar_init(&hdr->full[s], 1);
+        mbar_init(&hdr->empty[s], 1);
+      }
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&hdr->acc_full[b], 1);
+        mbar_init(&hdr->acc_empty[b], kDenseEpiWarps);
+      }
+      mbar_init(&hdr->drain, 1);
+      abort_flag[0] = 0;
+      abort_flag[1] = 0;
+      fence_mbar_init();
+      pdl_wait();
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      for (int s = 0; s < p.stages && kb0 + s * p.stage_blocks < kb1; ++s) load(s, kb0 + s * p.stage_blocks);
     }
-    mbar_init(&hdr->drain, 1);
-    abort_flag[0] = 0;
-    abort_flag[1] = 0;
-    fence_mbar_init();
-  }
-  if (warp == 8 && lane == 0) {
-    prefetch_tensormap(&tx);
-    prefetch_tensormap(&tw);
+    __syncwarp();
   }
   pdl_wait();
   if (warp == 9) tmem_alloc(&hdr->tmem, Cfg::kCols);
@@ -296,21 +313,12 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
 
   if (warp == 8) {
     if (elect_one()) {
-      asm volatile("fence.proxy.async.global;" ::: "memory");
       int stage = 0;
-      uint32_t phase = 0;
-      int issued = 0;
-      for (int kb = kb0; kb < kb1; kb += p.stage_blocks) {
-        if (!mbar_wait(&hdr->empty[stage], phase ^ 1u, abort_flag, nullptr, 0)) break;
-        uint8_t* sa = ring + stage * stage_bytes;
-        const bool two = p.stage_blocks == 2 && kb + 1 < kb1;
-        mbar_arrive_expect_tx(&hdr->full[stage], two ? 2 * block_bytes : block_bytes);
-        tma_load_2d(sa + a_bytes, &tw, &hdr->full[stage], kb * 128, n0);
-        tma_load_2d(sa, &tx, &hdr->full[stage], kb * 128, static_cast<int>(m0));
-        if (two) {
-          tma_load_2d(sa + block_bytes + a_bytes, &tw, &hdr->full[stage], kb * 128 + 128, n0);
-          tma_load_2d(sa + block_bytes, &tx, &hdr->full[stage], kb * 128 + 128, static_cast<int>(m0));
-        }
+      uint32_t phase = 0;                     // of the loads that a stage's MMAs make room for
+      int issued = p.stages;
+      for (int kb = kb0 + p.stages * p.stage_blocks; kb < kb1; kb += p.stage_blocks) {
+        if (!mbar_wait(&hdr->empty[stage], phase, abort_flag, nullptr, 0)) break;
+        load(stage, kb);
         ++issued;
         if (++stage == p.stages) {
           stage = 0;
@@ -319,7 +327,8 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
       }
       if (*abort_flag) {
         // the copies in flight land before the shared memory is given up
-        for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
+        for (int i = issued - p.stages; i < issued; ++i) {
+          if (kb0 + i * p.stage_blocks >= kb1) break;     // the last CTA's share may be a load short of the ring
           const unsigned long long t0 = globaltimer_ns();
           while (!mbar_test(&hdr->full[i % p.stages], (i / p.stages) & 1))
             if (globaltimer_ns() - t0 > kWaitLimitNs) break;
