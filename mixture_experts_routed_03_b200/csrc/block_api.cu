@@ -274,36 +274,46 @@ struct WarpsPlan {
 };
 
 // Tile and K split of dense_warps_kernel by estimated time: launch and join,
-// the rounds of loads, the CTAs on an SM, the bytes from HBM and those from L2.
-// A fit (9 % rms) to timings of 204 sizes from 4 x 128 x 256 to 2048 x 256 x
-// 16384 at every split, and 650 ns, by which plan_dense's estimates of small
-// calls are longer than their kernels; by the lesser of the two the choice
-// takes 2.5 % longer than the best one on average, 19 % at most.
+// the rounds of loads (and, of integers, their way to FP16), the CTAs on an SM,
+// the bytes from HBM and those from L2.  Fits (9 and 10 % rms) to timings of 204
+// sizes from 4 x 128 x 256 to 2048 x 256 x 16384 in BF16 and 201 from 3 x 64 x
+// 16384 to 256 x 20000 x 128 in integers at every split, and 650 and 1000 ns, by
+// which plan_dense's estimates of small calls are longer than their kernels; by
+// the lesser of the two the choice takes 2.5 and 1.6 % longer than the best one
+// on average, 19 and 33 % at most.
+template <int KIND>
 WarpsPlan plan_warps(int64_t M, int N, int64_t k_bytes, int sms) {
+  constexpr bool i8 = KIND == KIND_I8;
   WarpsPlan best{1, 1, 1e300};
-  const int groups = static_cast<int>(k_bytes / kWarpsGroup);
-  for (int xt = 1; xt <= 4; xt += 3) {
+  const int groups = static_cast<int>((k_bytes + kWarpsGroup - 1) / kWarpsGroup);
+  for (int xt = 1; xt <= kWarpsTall<KIND>; xt += kWarpsTall<KIND> - 1) {
     const int64_t tiles = (M + 8 * xt - 1) / (8 * xt) * ((N + 15) / 16);
     for (int s = 1; s <= 8; s *= 2) {
       if ((s > 1 && groups < 4 * s) || tiles * s > int64_t(16) * sms) break;
-      const int64_t slots = int64_t(cluster_slots(s, sms)) * warps_blocks(xt);
+      const int64_t slots = int64_t(cluster_slots(s, sms)) * warps_blocks<KIND>(xt);
       const double waves = static_cast<double>((tiles * s + slots - 1) / slots);
       const double per_sm = static_cast<double>((tiles * s + sms - 1) / sms);
       const double rounds = ((groups + s - 1) / s + kFewWarps - 1) / kFewWarps;
-      const double cost = 1380.0 + (s > 1 ? 886.0 : 0.0) + rounds * (133.0 * per_sm + 52.0 * waves * (xt + 2)) +
-                          363.0 * waves + 119.0 * per_sm * xt +
-                          static_cast<double>(k_bytes) * (30e-6 * (M + N) + 22e-6 * (16 + 8 * xt) * tiles);
+      const double hbm = static_cast<double>(k_bytes) * (M + N);
+      const double l2 = static_cast<double>(k_bytes) * (16 + 8 * xt) * tiles;
+      double cost;
+      if (i8)
+        cost = 1730.0 + (s > 1 ? 896.0 : 0.0) + rounds * 520.0 * waves + 402.0 * waves + 184.0 * per_sm * xt +
+               176e-6 * hbm + 57e-6 * l2;
+      else
+        cost = 1380.0 + (s > 1 ? 886.0 : 0.0) + rounds * (133.0 * per_sm + 52.0 * waves * (xt + 2)) + 363.0 * waves +
+               119.0 * per_sm * xt + 30e-6 * hbm + 22e-6 * l2;
       if (cost < best.cost) best = {xt, s, cost};
     }
   }
   return best;
 }
 
-template <int XT, int S>
+template <int KIND, int XT, int S>
 cudaError_t launch_warps(const FewArgs& a, cudaStream_t st) {
   const int n_tiles = (a.N + 15) / 16;
-  return launch_k(dense_warps_kernel<XT, S>, (a.M + 8 * XT - 1) / (8 * XT) * n_tiles * S, kFewWarps * 32, 0, st, a,
-                  n_tiles);
+  return launch_k(dense_warps_kernel<KIND, XT, S>, (a.M + 8 * XT - 1) / (8 * XT) * n_tiles * S, kFewWarps * 32, 0, st,
+                  a, n_tiles);
 }
 
 template <int KIND, int MB, int R, int D>
@@ -351,18 +361,20 @@ moe_status_t run_few(const FewArgs& a, int sms, cudaStream_t st) {
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-moe_status_t run_warps(const WarpsPlan& pl, const FewArgs& a, cudaStream_t st) {
-  cudaError_t e;
-  switch (pl.xt * 10 + pl.splits) {
-    case 11: e = launch_warps<1, 1>(a, st); break;
-    case 12: e = launch_warps<1, 2>(a, st); break;
-    case 14: e = launch_warps<1, 4>(a, st); break;
-    case 18: e = launch_warps<1, 8>(a, st); break;
-    case 41: e = launch_warps<4, 1>(a, st); break;
-    case 42: e = launch_warps<4, 2>(a, st); break;
-    case 44: e = launch_warps<4, 4>(a, st); break;
-    default: e = launch_warps<4, 8>(a, st); break;
+template <int KIND, int XT>
+cudaError_t run_warps_split(int splits, const FewArgs& a, cudaStream_t st) {
+  switch (splits) {
+    case 1: return launch_warps<KIND, XT, 1>(a, st);
+    case 2: return launch_warps<KIND, XT, 2>(a, st);
+    case 4: return launch_warps<KIND, XT, 4>(a, st);
+    default: return launch_warps<KIND, XT, 8>(a, st);
   }
+}
+
+template <int KIND>
+moe_status_t run_warps(const WarpsPlan& pl, const FewArgs& a, cudaStream_t st) {
+  const cudaError_t e = pl.xt == 1 ? run_warps_split<KIND, 1>(pl.splits, a, st)
+                                   : run_warps_split<KIND, kWarpsTall<KIND>>(pl.splits, a, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -415,13 +427,13 @@ moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_byt
   if (p.M <= kFewMaxM<KIND>) return run_few<KIND>(few_args(p, x, w, k_bytes, x_stride, w_stride), sms, st);
   p.k_blocks = static_cast<int>((k_bytes + 127) / 128);
   const DensePlan pl = plan_dense<KIND>(p.M, p.N, p.k_blocks, sms);
+  const WarpsPlan pw = plan_warps<KIND>(p.M, p.N, k_bytes, sms);
   if (KIND == KIND_I8) {
     const DensePlan pp = plan_pair(p.M, p.N, p.k_blocks, sms);
-    if (pp.cost < pl.cost) return run_pair(p, pp.nt, x, w, k_bytes, x_stride, w_stride, sms, st);
-  } else {
-    const WarpsPlan pw = plan_warps(p.M, p.N, k_bytes, sms);
-    if (pw.cost < pl.cost) return run_warps(pw, few_args(p, x, w, k_bytes, x_stride, w_stride), st);
+    if (pp.cost < pl.cost && pp.cost < pw.cost)
+      return run_pair(p, pp.nt, x, w, k_bytes, x_stride, w_stride, sms, st);
   }
+  if (pw.cost < pl.cost) return run_warps<KIND>(pw, few_args(p, x, w, k_bytes, x_stride, w_stride), st);
   p.splits = pl.splits;
   p.tile_rows = pl.tile_rows;
   CUtensorMap tx, tw;

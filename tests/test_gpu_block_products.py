@@ -116,6 +116,40 @@ def test_int8_single_row_of_odd_length():
     _check(lin.forward(case[0].to(DEV), case[1].to(DEV)), case, True)
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 1, 1), (16, 100, 2048), (9, 1001, 100), (5, 17, 4096), (48, 255, 4096),
+                                   (5, 1000, 4111), (24, 1, 131071), (9, 128, 16384), (24, 1000, 512), (300, 61, 15),
+                                   (17, 1001, 2049), (300, 60, 7168), (64, 257, 4100), (24, 256, 16384), (13, 1000, 7175),
+                                   (48, 60, 8192), (24, 100, 16399), (3, 2048, 2048), (31, 2048, 2048)])
+@pytest.mark.parametrize("codes", ["any", "least", "ends"])
+def test_int8_product_of_a_batch(M, N, K, codes):
+    """The warps' MMAs at every split of K and height of tile; codes whose products and sums are the largest there are."""
+    x, xs, w, ws, b = _case(M, N, K, seed=M + N)
+    if codes == "least":
+        x, w = torch.full_like(x, -128), torch.full_like(w, -128)
+    elif codes == "ends":
+        x, w = (torch.where(t < 0, -128, 127).to(torch.int8) for t in (x, w))
+    stride = -(-K // 16) * 16
+    out = torch.full((M + 1, N + 3), 5.0, device=DEV)
+    status = _status()
+    api.matmul_int8(api.int8_problem(M, K, N, True, x_stride=stride, w_stride=stride, out_stride=N + 3),
+                    _padded(x, stride), xs.to(DEV), _padded(w, stride), ws.to(DEV), out, status, bias=b.to(DEV))
+    _check(out[:M, :N], (x, xs, w, ws, b), True)
+    assert (out[M] == 5).all() and (out[:M, N:] == 5).all() and int(status.item()) == api.MOE_OK
+
+
+def test_int8_rows_that_end_with_their_memory():
+    """Rows of odd length in memory that ends with the last of them: nothing behind it may matter."""
+    M, N, K, stride = 9, 40, 141, 144
+    x, xs, w, ws, b = _case(M, N, K, seed=41)
+    bx, bw = (torch.full(((t.shape[0] - 1) * stride + K,), 99, dtype=torch.int8, device=DEV) for t in (x, w))
+    for t, buf in ((x, bx), (w, bw)):
+        torch.as_strided(buf, (t.shape[0], K), (stride, 1)).copy_(t)
+    out = torch.empty((M, N), device=DEV)
+    api.matmul_int8(api.int8_problem(M, K, N, True, x_stride=stride, w_stride=stride), bx, xs.to(DEV), bw, ws.to(DEV), out,
+                    _status(), bias=b.to(DEV))
+    _check(out, (x, xs, w, ws, b), True)
+
+
 def test_int8_scales_that_are_not_finite_follow_the_arithmetic():
     case = _case(6, 40, 64, seed=4)
     xs = case[1].clone()
