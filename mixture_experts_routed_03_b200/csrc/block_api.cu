@@ -159,10 +159,8 @@ int dense_fixed_bytes(int block) { return 1024 + kDenseHeader + (block < 128 * 1
 
 // k blocks per stage.  Two while they are small: a wait, a commit and a
 // barrier's arming for every eight MMAs.  Two also for BF16 tiles of 128
-// columns that each have an SM and the whole K axis to themselves (8192 x 256
-// x 2048: 14.5 us against 18.5); with a second CTA on the SM, which then does
-// not fit, or a part of K, one is faster (16384 x 128 x 4096, K in two: 30
-// against 36).
+// columns that have the whole K axis to themselves (8192 x 256 x 2048: 14.5 us
+// against 18.5).
 int dense_stage_blocks(int kind, int rows, int nt, int splits, int64_t ctas, int sms) {
   if (rows + nt <= 128) return 2;
   return kind == KIND_BF16 && nt == 128 && splits == 1 && ctas <= sms ? 2 : 1;
@@ -178,33 +176,27 @@ template <int KIND>
 DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
   constexpr int kWidest = KIND == KIND_I8 ? 256 : 128;
   DensePlan best{0, kWidest, 1, 128, 1e300};
-  for (int nt = kWidest; nt >= 32; nt /= 2) {
+  for (int nt = kWidest; nt >= kDenseNarrowest<KIND>; nt /= 2) {
     const int64_t n_tiles = (N + nt - 1) / nt;
     for (int s = 1; s <= 8; s *= 2) {
       if (s > 1 && k_blocks < 4 * s) break;
       // as many row tiles as the last wave has room for, none higher than 128
       const int64_t mt0 = (M + 127) / 128;
-      const int blk0 = (M >= 128 ? 128 : static_cast<int>((M + 7) / 8 * 8)) + nt;
-      const int stage0 = blk0 * 128 * dense_stage_blocks(KIND, blk0 - nt, nt, s, mt0 * n_tiles * s, sms);
-      int res = 1;
-      const int half = kDenseHalfSmemBytes - dense_fixed_bytes(blk0 * 128);
-      if (mt0 * n_tiles * s > sms && half >= 3 * stage0) res = 2;
-      const int64_t slots = int64_t(cluster_slots(s, sms)) * res;
+      const int64_t slots = cluster_slots(s, sms);
+      if (s > 1 && mt0 * n_tiles * s > slots) break;   // clusters only as many as run at once
       const int64_t waves = (mt0 * n_tiles * s + slots - 1) / slots;
       int64_t mt = waves * slots / (n_tiles * s);
       if (mt < mt0) mt = mt0;
-      int64_t rows = ((M + mt - 1) / mt + 7) / 8 * 8;
+      int64_t rows = ((M + mt - 1) / mt + 15) / 16 * 16;
       if (rows > 128) rows = 128;
       mt = (M + rows - 1) / rows;
       const int64_t ctas = mt * n_tiles * s;
-      const int64_t per_sm = (ctas + sms - 1) / sms;
-      const double live = per_sm < res ? static_cast<double>(per_sm) : res;
       const double issue = 195.0 / dense_stage_blocks(KIND, static_cast<int>(rows), nt, s, ctas, sms) + 90.0;
-      const double load = live * (rows + nt) * 128.0 / 127.0;
-      const double mma = live * nt * 1.05;
+      const double load = (rows + nt) * 128.0 / 127.0;
+      const double mma = nt * 1.05;
       const double block = issue > load ? (issue > mma ? issue : mma) : (load > mma ? load : mma);
       const int64_t blocks = (k_blocks + s - 1) / s;
-      double cost = 1200.0 + waves * (blocks * block + 1800.0 + 0.14 * rows * nt / s * live +
+      double cost = 1200.0 + waves * (blocks * block + 1800.0 + 0.14 * rows * nt / s +
                                       (s > 1 ? 1200.0 * std::sqrt(static_cast<double>(s)) : 0.0));
       const double memory = 3000.0 + static_cast<double>(M + N) * k_blocks * 128.0 / 6000.0;
       if (cost < memory) cost = memory;
@@ -238,12 +230,7 @@ cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap&
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const int block = (p.tile_rows + NT) * 128, stage = block * p.stage_blocks;
   const int fixed = dense_fixed_bytes(block);
-  // two CTAs an SM where there are more than SMs and a ring of three stages
-  // fits in half of the shared memory
-  int room = kDenseSmemBytes - fixed;
-  const int half = kDenseHalfSmemBytes - fixed;
-  if (grid > sms && half >= 3 * stage) room = half;
-  p.stages = room / stage;
+  p.stages = (kDenseSmemBytes - fixed) / stage;
   if (p.stages > kDenseMaxStages) p.stages = kDenseMaxStages;
   const int per_cta = ((p.k_blocks + p.splits - 1) / p.splits + p.stage_blocks - 1) / p.stage_blocks;
   if (p.stages > per_cta) p.stages = per_cta;
@@ -442,7 +429,7 @@ moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_byt
     return MOE_ERR_CUDA;
   cudaError_t e;
   switch (pl.nt) {
-    case 32: e = launch_dense<KIND, 32>(p, tx, tw, sms, st); break;
+    case 32: e = launch_dense<KIND, kDenseNarrowest<KIND>>(p, tx, tw, sms, st); break;   // integers alone
     case 64: e = launch_dense<KIND, 64>(p, tx, tw, sms, st); break;
     case 128: e = launch_dense<KIND, 128>(p, tx, tw, sms, st); break;
     default: e = launch_dense<KIND, KIND == KIND_I8 ? 256 : 128>(p, tx, tw, sms, st); break;
@@ -457,7 +444,7 @@ cudaError_t set_dense_attr() {
 
 template <int KIND>
 cudaError_t set_dense_attrs() {
-  cudaError_t e = set_dense_attr<KIND, 32>();
+  cudaError_t e = set_dense_attr<KIND, kDenseNarrowest<KIND>>();
   if (e == cudaSuccess) e = set_dense_attr<KIND, 64>();
   if (e == cudaSuccess) e = set_dense_attr<KIND, 128>();
   if (e == cudaSuccess && KIND == KIND_I8) e = set_dense_attr<KIND_I8, 256>();

@@ -18,10 +18,13 @@
 // out the tile's elements: each is summed over the ranks in their order through
 // distributed shared memory (so results do not depend on timing; no workspace,
 // no atomics), scaled and stored; the cluster meets again before any CTA
-// leaves.  (Partials written into their owners' memory instead, with nothing
-// remote after the one meeting, took half a microsecond less at 64 x 256 x 7168
-// but faulted now and then where two CTAs shared an SM; the cause was not found
-// by reading, so it is not done.)
+// leaves.
+//
+// A CTA has its SM for itself, BF16 tiles are at least 64 columns wide and
+// tiles a multiple of 16 rows high.  Two CTAs an SM raised an illegal address
+// four times in some thousand calls with BF16 tiles of 72 x 32 (K split or not,
+// 88 or 112 KB of shared memory each) and in no others; the cause was not found
+// by reading, so nothing that those calls had in common is done.
 //
 // Of BF16 the tensor cores truncate as they add to the accumulator, so a
 // sum's error grows with the number of MMAs behind it (4.4e-6 relative after
@@ -36,8 +39,8 @@
 // TMEM is allocated after griddepcontrol.wait and dependents are released
 // after the allocation: a CTA of this kernel never holds tensor memory while
 // it waits for another grid, and a later grid's CTA cannot take what this
-// one still needs.  kDenseMinSmemBytes keeps it at two CTAs an SM, whose
-// allocations fit together, and off the SMs that the grouped GEMMs hold.
+// one still needs.  kDenseMinSmemBytes keeps a CTA alone on its SM, and off the
+// SMs that the grouped GEMMs hold.
 //
 // Every wait is bounded; a wait that runs out raises the CTA's abort flag,
 // the status word gets MOE_ERR_TIMEOUT, copies and MMAs in flight are waited
@@ -54,10 +57,14 @@ constexpr int kDenseEpiWarps = 8;
 constexpr int kDenseThreads = (kDenseEpiWarps + 2) * 32;
 constexpr int kDenseEpiThreads = kDenseEpiWarps * 32;
 constexpr int kDenseMaxStages = 24;
+// Stages loaded before the block meets.  (333 x 1001 x 1040: none 4.84 us, 2 4.65,
+// all 5.02; 64 x 7168 x 2048: 6.75, 6.45 and 6.56.)
+constexpr int kDenseEarly = 2;
 constexpr int kDenseHeader = 4096;            // barriers, flags, the tile's scales
 constexpr int kDenseSmemBytes = 220 * 1024;   // at most
-constexpr int kDenseHalfSmemBytes = 112 * 1024;   // two CTAs an SM
-constexpr int kDenseMinSmemBytes = 80 * 1024;
+constexpr int kDenseMinSmemBytes = 120 * 1024;   // at least: one CTA an SM
+template <int KIND>
+constexpr int kDenseNarrowest = KIND == KIND_I8 ? 32 : 64;   // columns of a tile
 
 struct DenseArgs {
   int64_t M;
@@ -65,7 +72,7 @@ struct DenseArgs {
   int k_blocks;            // ceil(K bytes / 128)
   int splits;              // CTAs per cluster
   int n_tiles;
-  int tile_rows;           // output rows per tile: a multiple of 8, at most 128
+  int tile_rows;           // output rows per tile: a multiple of 16, at most 128
   int stages;
   int stage_blocks;        // k blocks per stage, 1 or 2
   int out_fp32;
@@ -270,6 +277,8 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
 
   // The ring's first loads wait for nothing but the barriers that the loading
   // thread sets up itself: they are under way while tensor memory is allocated.
+  // Only as many as that takes: the other warps wait for them to be issued.
+  const int early = p.stages < kDenseEarly ? p.stages : kDenseEarly;
   auto load = [&](int stage, int kb) {
     uint8_t* sa = ring + stage * stage_bytes;
     const bool two = p.stage_blocks == 2 && kb + 1 < kb1;
@@ -299,7 +308,7 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
       fence_mbar_init();
       pdl_wait();
       asm volatile("fence.proxy.async.global;" ::: "memory");
-      for (int s = 0; s < p.stages && kb0 + s * p.stage_blocks < kb1; ++s) load(s, kb0 + s * p.stage_blocks);
+      for (int s = 0; s < early && kb0 + s * p.stage_blocks < kb1; ++s) load(s, kb0 + s * p.stage_blocks);
     }
     __syncwarp();
   }
@@ -313,11 +322,11 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
 
   if (warp == 8) {
     if (elect_one()) {
-      int stage = 0;
-      uint32_t phase = 0;                     // of the loads that a stage's MMAs make room for
-      int issued = p.stages;
-      for (int kb = kb0 + p.stages * p.stage_blocks; kb < kb1; kb += p.stage_blocks) {
-        if (!mbar_wait(&hdr->empty[stage], phase, abort_flag, nullptr, 0)) break;
+      int stage = early < p.stages ? early : 0;
+      uint32_t phase = early < p.stages ? 0 : 1;
+      int issued = early;
+      for (int kb = kb0 + early * p.stage_blocks; kb < kb1; kb += p.stage_blocks) {
+        if (!mbar_wait(&hdr->empty[stage], phase ^ 1u, abort_flag, nullptr, 0)) break;
         load(stage, kb);
         ++issued;
         if (++stage == p.stages) {
@@ -327,8 +336,8 @@ __global__ void __launch_bounds__(kDenseThreads, 2)
       }
       if (*abort_flag) {
         // the copies in flight land before the shared memory is given up
-        for (int i = issued - p.stages; i < issued; ++i) {
-          if (kb0 + i * p.stage_blocks >= kb1) break;     // the last CTA's share may be a load short of the ring
+        for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
+          if (kb0 + i * p.stage_blocks >= kb1) break;     // a share of K that is shorter than `early`
           const unsigned long long t0 = globaltimer_ns();
           while (!mbar_test(&hdr->full[i % p.stages], (i / p.stages) & 1))
             if (globaltimer_ns() - t0 > kWaitLimitNs) break;
