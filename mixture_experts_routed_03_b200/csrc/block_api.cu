@@ -166,15 +166,15 @@ int dense_stage_blocks(int kind, int rows, int nt, int splits, int64_t ctas, int
   return kind == KIND_BF16 && nt == 128 && splits == 1 && ctas <= sms ? 2 : 1;
 }
 
-// Tile and K split of dense_kernel by estimated time: whole waves of CTAs,
-// each its share of the k blocks at the slowest of issue, loads and MMAs,
+// Tile and K split of dense_kernel by estimated time: whole waves of CTAs, one
+// an SM, each its share of the k blocks at the slowest of issue, loads and MMAs,
 // plus what a tile costs besides.  The constants are a fit to timings of 32
 // sizes, from 1 x 60 x 2048 to 16384 x 128 x 8192 bytes, at every width and
-// split; of 28 sizes timed again (these and the CTA pairs) the choice is the
-// fastest or within 5 % of it for 22, and within 15 % for the others.
+// split.  (256 columns in BF16: 16384 x 256 x 7168 66 us, 98 in two tiles of 128;
+// 1000 x 256 x 7168 12.9 and 15.5.)
 template <int KIND>
 DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
-  constexpr int kWidest = KIND == KIND_I8 ? 256 : 128;
+  constexpr int kWidest = 256;
   DensePlan best{0, kWidest, 1, 128, 1e300};
   for (int nt = kWidest; nt >= kDenseNarrowest<KIND>; nt /= 2) {
     const int64_t n_tiles = (N + nt - 1) / nt;
@@ -432,7 +432,7 @@ moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_byt
     case 32: e = launch_dense<KIND, kDenseNarrowest<KIND>>(p, tx, tw, sms, st); break;   // integers alone
     case 64: e = launch_dense<KIND, 64>(p, tx, tw, sms, st); break;
     case 128: e = launch_dense<KIND, 128>(p, tx, tw, sms, st); break;
-    default: e = launch_dense<KIND, KIND == KIND_I8 ? 256 : 128>(p, tx, tw, sms, st); break;
+    default: e = launch_dense<KIND, 256>(p, tx, tw, sms, st); break;
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -447,7 +447,7 @@ cudaError_t set_dense_attrs() {
   cudaError_t e = set_dense_attr<KIND, kDenseNarrowest<KIND>>();
   if (e == cudaSuccess) e = set_dense_attr<KIND, 64>();
   if (e == cudaSuccess) e = set_dense_attr<KIND, 128>();
-  if (e == cudaSuccess && KIND == KIND_I8) e = set_dense_attr<KIND_I8, 256>();
+  if (e == cudaSuccess) e = set_dense_attr<KIND, 256>();
   return e;
 }
 

@@ -139,7 +139,7 @@ struct DenseCfg {
   static constexpr int kChunk = KIND == KIND_I8 ? (1 << 30) : 4;   // k blocks (of 4 MMAs) until one is emptied
   static constexpr int kCols = NT * kBufs;
   static constexpr int kPitch = NT * 4 + 16;                 // bytes of a staged row: 16 more spread the banks
-  static_assert(kCols >= 32 && kCols <= 256, "TMEM columns");
+  static_assert(kCols >= 32 && kCols <= 512, "TMEM columns");
 };
 
 struct DenseHeader {
@@ -251,7 +251,7 @@ __device__ __forceinline__ void join_and_store(const DenseArgs& p, const DenseHe
 }
 
 template <int KIND, int NT>
-__global__ void __launch_bounds__(kDenseThreads, 2)
+__global__ void __launch_bounds__(kDenseThreads, 1)
     dense_kernel(const __grid_constant__ DenseArgs p, const __grid_constant__ CUtensorMap tx,
                  const __grid_constant__ CUtensorMap tw) {
   using Cfg = DenseCfg<KIND, NT>;
