@@ -9,8 +9,8 @@
 // dense_kernel: one output tile of up to 128 rows and NT columns per cluster
 // of S CTAs, which split the K axis.  Operands come by TMA, 128 bytes of K a
 // block (128-byte swizzle, K-major), rows and columns past the ends filled
-// with zeros; x rows only as many as the tile has (a multiple of the
-// swizzle's 8), since the accumulator rows of what lies behind them are never
+// with zeros; x rows only as many as the tile has (whole groups
+// of the swizzle's 8), since the accumulator rows of what lies behind them are never
 // read -- so the row tiles are cut to fill the last wave of SMs.  Warp 8 loads,
 // warp 9 issues the MMAs into TMEM, warps 0-7 (two per 32-lane TMEM quarter,
 // one per half of the columns) take the sums out.  Then each CTA leaves its
