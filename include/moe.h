@@ -254,7 +254,9 @@ moe_status_t moe_workspace_init(void* workspace, size_t workspace_bytes, void* s
  * degrade silently -- here, a CTA that never arrives must surface as an
  * error, not as a hang).  wait_limit_us > 0 makes every bounded wait of
  * later calls on this workspace give up after that many microseconds
- * instead of 2 s (0 restores the default).  skip_arrival = 1 makes CTA 0 of
+ * instead of 2 s (0 restores the default; moe_router_logits, which takes a
+ * workspace for its status word alone, and moe_matmul_int8 go by
+ * moe_product_test_hooks instead).  skip_arrival = 1 makes CTA 0 of
  * the next moe_fused call withhold its arrival at its first grid barrier,
  * once: the other CTAs' waits run out, the call returns, the status word
  * reads MOE_ERR_TIMEOUT and the outputs are unspecified.  Nothing faults or
@@ -489,6 +491,21 @@ typedef struct {
 moe_status_t moe_matmul_int8(const moe_int8_matmul_t* problem, const int8_t* x, const float* x_scale,
                              const int8_t* w, const float* w_scale, const float* bias, void* out,
                              int32_t* device_status, void* stream);
+
+/* Test hook of the products' failure detection, on the host: for calls of
+ * moe_router_logits and moe_matmul_int8 enqueued (or captured) by this process
+ * from now on, a wait limit in microseconds for every bounded wait (0: the
+ * default of 2 s) and an event that never comes, so that the waits for it run
+ * out and the call's device_status becomes MOE_ERR_TIMEOUT.  It reaches the
+ * tcgen05 kernels; those of a few rows have no waits.  (0, MOE_HOLD_NOTHING)
+ * ends it.  Nothing on the device is left behind: the next call is right. */
+typedef enum {
+  MOE_HOLD_NOTHING = 0,
+  MOE_HOLD_LOAD = 1,             /* the last operand load of the first CTA */
+  MOE_HOLD_SUM = 2,              /* the hand-over of its last sum */
+  MOE_HOLD_LOAD_OF_SECOND = 3    /* the last operand load of the second CTA */
+} moe_product_hold_t;
+moe_status_t moe_product_test_hooks(int32_t wait_limit_us, int32_t hold);
 
 /* Where moe_fused leaves its working data inside the workspace, for
  * inspection and testing: byte offsets from the workspace base for a call

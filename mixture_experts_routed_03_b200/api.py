@@ -41,7 +41,7 @@ EXPORTS = (
     "moe_fused", "moe_read_status", "moe_status_string", "moe_timing_enable", "moe_timing_read",
     "moe_permute_noalloc", "moe_get_tile_regime", "moe_get_workspace_offsets",
     "moe_workspace_test_hooks", "moe_quantize_nvfp4_rowwise",
-    "moe_rmsnorm_quantize", "moe_router_logits", "moe_matmul_int8",
+    "moe_rmsnorm_quantize", "moe_router_logits", "moe_matmul_int8", "moe_product_test_hooks",
 )
 
 SLOTS = ("route", "permute", "gather", "gemm1", "zero", "gemm2", "finalize", "combine", "fused")
@@ -167,6 +167,7 @@ def lib():
             "moe_rmsnorm_quantize": [ctypes.POINTER(NormProblem)] + [vp] * 9,
             "moe_router_logits": [P, vp, vp, vp, vp, vp],
             "moe_matmul_int8": [ctypes.POINTER(Int8Problem)] + [vp] * 8,
+            "moe_product_test_hooks": [i32, i32],
             "moe_prepare_weights": [P, ctypes.POINTER(Weights), vp, vp, vp],
             "moe_get_prepared_weights_size": [P, ctypes.POINTER(sz), ctypes.POINTER(sz)],
             "moe_route": [P, vp, vp, vp, vp, vp],
@@ -230,6 +231,7 @@ def _check(fn, code):
 
 TILE_REGIMES = {"auto": 0, "large_m": 1, "small_m": 2}
 ACTIVATIONS = {"swiglu": 0, "swigluoai": 1}
+PRODUCT_HOLDS = {"nothing": 0, "load": 1, "sum": 2, "load_of_second": 3}
 NORM_FORMATS = {"bf16": 0, "fp8": 1, "mxfp8": 3, "fp8_tensor": 4, "int8": 5}
 
 
@@ -385,6 +387,14 @@ def matmul_int8(prob, x, x_scale, w, w_scale, out, device_status, bias=None, str
     code = call(at, ctypes.addressof(prob), x, x_scale, w, w_scale, bias, out, device_status, _stream(stream))
     if code:
         raise MoEError("moe_matmul_int8", code)
+
+
+def product_test_hooks(wait_limit_us=0, hold="nothing"):
+    """Test hook of the products' failure detection: a wait limit and an event
+    that never comes, for calls from now on (see include/moe.h); no arguments
+    end it.  hold: a PRODUCT_HOLDS name or code."""
+    code = PRODUCT_HOLDS[hold] if isinstance(hold, str) else int(hold)
+    _check("moe_product_test_hooks", lib().moe_product_test_hooks(int(wait_limit_us), code))
 
 
 def permute(prob, topk_idx, lay, ws, ws_bytes, stream=None):

@@ -3,6 +3,7 @@
 // the activation encodings, the router's logits, and the product in 8-bit
 // integers.  Argument checks, TMA descriptors and launches; no memory is
 // allocated here.
+#include <atomic>
 #include <cstring>
 
 #include "dense.cuh"
@@ -31,6 +32,9 @@ struct Range {
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int64_t kMaxStride = int64_t(1) << 31;   // rows x strides x 4 bytes stay below 2^63
+
+// moe_product_test_hooks
+std::atomic<int> hook_wait_limit_us{0}, hook_withhold{MOE_HOLD_NOTHING};
 
 // ---------------------------------------------------------------- norm
 constexpr int kNormMaxHidden = 32768;   // 1024 threads x 4 vectors of 8
@@ -423,6 +427,8 @@ moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_byt
   if (pw.cost < pl.cost) return run_warps<KIND>(pw, few_args(p, x, w, k_bytes, x_stride, w_stride), st);
   p.splits = pl.splits;
   p.tile_rows = pl.tile_rows;
+  p.wait_limit_us = hook_wait_limit_us.load(std::memory_order_relaxed);
+  p.withhold = hook_withhold.load(std::memory_order_relaxed);
   CUtensorMap tx, tw;
   if (!make_dense_map(&tx, x, k_bytes, p.M, x_stride, p.tile_rows) ||
       !make_dense_map(&tw, w, k_bytes, p.N, w_stride, pl.nt))
@@ -606,6 +612,13 @@ moe_status_t moe_matmul_int8(const moe_int8_matmul_t* p, const int8_t* x, const 
   a.vec = aligned(out, 4 * ob) && os % 4 == 0;
   a.status = device_status;
   return run_dense<KIND_I8>(a, x, w, K, xs, ws, static_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_product_test_hooks(int32_t wait_limit_us, int32_t hold) {
+  if (wait_limit_us < 0 || hold < MOE_HOLD_NOTHING || hold > MOE_HOLD_LOAD_OF_SECOND) return MOE_ERR_INVALID_ARG;
+  hook_wait_limit_us.store(wait_limit_us, std::memory_order_relaxed);
+  hook_withhold.store(hold, std::memory_order_relaxed);
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -42,9 +42,11 @@
 // one still needs.  kDenseMinSmemBytes keeps a CTA alone on its SM, and off the
 // SMs that the grouped GEMMs hold.
 //
-// Every wait is bounded; a wait that runs out raises the CTA's abort flag,
-// the status word gets MOE_ERR_TIMEOUT, copies and MMAs in flight are waited
-// for (bounded too) and the outputs are not written.
+// Every wait is bounded; a wait that runs out raises the CTA's abort flag.  The
+// flags are final once the cluster has met: if one is raised, no CTA of the
+// cluster stores, the status word gets MOE_ERR_TIMEOUT, and each CTA waits
+// (bounded too) for its copies and MMAs in flight before they meet again and
+// give shared and tensor memory up.
 #pragma once
 
 #include "common.cuh"
@@ -83,6 +85,8 @@ struct DenseArgs {
   void* out;
   int64_t out_stride;      // elements
   int* status;
+  int wait_limit_us;       // of every bounded wait; 0: the default (kWaitLimitNs)
+  int withhold;            // moe_product_hold_t
 };
 
 __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -147,6 +151,7 @@ struct DenseHeader {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;                            // after an abort: the MMAs issued are complete
   uint32_t tmem;
+  int issued;                                // loads, by the end of the loading thread's part
   alignas(16) volatile int abort_flag[4];    // raised, wait limit (0: the default); read 16 bytes at a time
   alignas(16) float xs[128], ws[256], bias[256];   // the tile's scales (KIND_I8)
 };
@@ -161,6 +166,13 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e != 0;
+}
+
+// Waits, as long as a wait may take, for what is in flight behind `bar` after an abort.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_test(bar, parity))
+    if (globaltimer_ns() - t0 > limit_ns_of(abort[1])) break;
 }
 
 template <int KIND>
@@ -274,11 +286,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   const uint32_t a_bytes = static_cast<uint32_t>(p.tile_rows) * 128u;
   const uint32_t block_bytes = a_bytes + NT * 128u;
   const uint32_t stage_bytes = block_bytes * p.stage_blocks;
+  // loads of this CTA, one less where a test withholds the last
+  const bool hold_load = (p.withhold == MOE_HOLD_LOAD && blockIdx.x == 0) ||
+                         (p.withhold == MOE_HOLD_LOAD_OF_SECOND && blockIdx.x == 1);
+  const int loads = (kb1 - kb0 + p.stage_blocks - 1) / p.stage_blocks - (hold_load ? 1 : 0);
 
   // The ring's first loads wait for nothing but the barriers that the loading
   // thread sets up itself: they are under way while tensor memory is allocated.
   // Only as many as that takes: the other warps wait for them to be issued.
-  const int early = p.stages < kDenseEarly ? p.stages : kDenseEarly;
+  int early = p.stages < kDenseEarly ? p.stages : kDenseEarly;
+  if (early > loads) early = loads;
   auto load = [&](int stage, int kb) {
     uint8_t* sa = ring + stage * stage_bytes;
     const bool two = p.stage_blocks == 2 && kb + 1 < kb1;
@@ -304,11 +321,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       }
       mbar_init(&hdr->drain, 1);
       abort_flag[0] = 0;
-      abort_flag[1] = 0;
+      abort_flag[1] = p.wait_limit_us;
       fence_mbar_init();
       pdl_wait();
       asm volatile("fence.proxy.async.global;" ::: "memory");
-      for (int s = 0; s < early && kb0 + s * p.stage_blocks < kb1; ++s) load(s, kb0 + s * p.stage_blocks);
+      for (int s = 0; s < early; ++s) load(s, kb0 + s * p.stage_blocks);
     }
     __syncwarp();
   }
@@ -325,24 +342,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       int stage = early < p.stages ? early : 0;
       uint32_t phase = early < p.stages ? 0 : 1;
       int issued = early;
-      for (int kb = kb0 + early * p.stage_blocks; kb < kb1; kb += p.stage_blocks) {
+      for (; issued < loads; ++issued) {
         if (!mbar_wait(&hdr->empty[stage], phase ^ 1u, abort_flag, nullptr, 0)) break;
-        load(stage, kb);
-        ++issued;
+        load(stage, kb0 + issued * p.stage_blocks);
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      if (*abort_flag) {
-        // the copies in flight land before the shared memory is given up
-        for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
-          if (kb0 + i * p.stage_blocks >= kb1) break;     // a share of K that is shorter than `early`
-          const unsigned long long t0 = globaltimer_ns();
-          while (!mbar_test(&hdr->full[i % p.stages], (i / p.stages) & 1))
-            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-        }
-      }
+      hdr->issued = issued;
     }
   } else if (warp == 9) {
     if (elect_one()) {
@@ -352,6 +360,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       uint32_t phase = 0;
       int in = 0, buf = 0;                    // k block of the chunk, accumulator buffer
       uint32_t buf_phase = 1;
+      const bool hold_sum = p.withhold == MOE_HOLD_SUM && blockIdx.x == 0;
       for (int kb = kb0; kb < kb1; kb += p.stage_blocks) {
         if (!mbar_wait(&hdr->full[stage], phase, abort_flag, nullptr, 0)) break;
         tc_fence_after();
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
           }
           ++in;
           if (Cfg::kBufs > 1 && (in == Cfg::kChunk || kb + b == kb1 - 1)) {
-            mma_commit(&hdr->acc_full[buf]);
+            if (!hold_sum || kb + b < kb1 - 1) mma_commit(&hdr->acc_full[buf]);
             in = 0;
             buf ^= 1;
             buf_phase ^= buf == 0;
@@ -390,13 +399,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
           phase ^= 1u;
         }
       }
-      if (Cfg::kBufs == 1) mma_commit(&hdr->acc_full[0]);
-      if (*abort_flag) {
-        mma_commit(&hdr->drain);
-        const unsigned long long t0 = globaltimer_ns();
-        while (!mbar_test(&hdr->drain, 0))
-          if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-      }
+      if (Cfg::kBufs == 1 && !hold_sum) mma_commit(&hdr->acc_full[0]);
     }
   } else {
     // epilogue: the tile's scales while the operands stream in, then the sums
@@ -461,14 +464,29 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     tc_fence_before();
   }
   __syncwarp();
-  // an abort anywhere in the cluster keeps all of it from storing
+  // An abort anywhere in the cluster keeps all of it from storing.  Only here
+  // are the flags final: a warp whose own part ended well may have been followed
+  // by another's time-out.
   if (S > 1) cluster_sync_all();
   else __syncthreads();
   __syncwarp();
   const uint32_t flag = smem_u32(const_cast<int*>(abort_flag));
   const bool raised = S == 1 ? *abort_flag != 0 : lane < S && ld_cluster16(mapa_rank(flag, lane)).x != 0;
   const bool ok = !__any_sync(0xFFFFFFFFu, raised);
-  if (!ok && threadIdx.x == 0) record_error(p.status, MOE_ERR_TIMEOUT);
+  if (!ok) {
+    if (threadIdx.x == 0) record_error(p.status, MOE_ERR_TIMEOUT);
+    // what is in flight ends before the memory it works on is given up
+    if (warp == 8 && elect_one()) {
+      const int issued = hdr->issued;
+      for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+        drain_wait(&hdr->full[i % p.stages], (i / p.stages) & 1, abort_flag);
+    }
+    if (warp == 9 && elect_one()) {     // the thread that issued the MMAs
+      mma_commit(&hdr->drain);
+      drain_wait(&hdr->drain, 0, abort_flag);
+    }
+    __syncwarp();
+  }
   if (ok && warp < kDenseEpiWarps) {
     switch (S) {
       case 1: join_and_store<KIND, NT, 1>(p, hdr, ring, rank, rows, m0, n0); break;

@@ -236,3 +236,16 @@ def test_binding_function_checks_its_own_arguments(lib):
     for args in ((), (at,), (at, 0), (at,) + (0,) * 13):
         with pytest.raises(TypeError):
             call(*args)
+
+
+# ------------------------------------------------------------------ the products' test hook
+
+def test_product_test_hooks_check_their_arguments(lib):
+    for bad in (dict(wait_limit_us=-1), dict(hold=-1), dict(hold=4)):
+        with pytest.raises(api.MoEError) as e:
+            api.product_test_hooks(**bad)
+        assert e.value.code == BAD
+    with pytest.raises(KeyError):
+        api.product_test_hooks(hold="everything")
+    api.product_test_hooks(5, "sum")
+    api.product_test_hooks()
