@@ -394,6 +394,8 @@ moe_status_t run_pair(const DenseArgs& p, int nt, const void* x, const void* w, 
   // lose what lies behind them
   a.vec = aligned16(p.out) && p.out_stride % per16 == 0 && p.N % per16 == 0;
   a.status = p.status;
+  a.wait_limit_us = p.wait_limit_us;
+  a.withhold = p.withhold;
   a.m_tiles = static_cast<int>((p.M + 255) / 256);
   a.n_tiles = (p.N + nt - 1) / nt;
   if (int64_t(a.m_tiles) * a.n_tiles > 0x7FFFFFFF - sms) return MOE_ERR_UNSUPPORTED;
@@ -417,6 +419,8 @@ moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_byt
   const int sms = sm_count();
   if (p.M <= kFewMaxM<KIND>) return run_few<KIND>(few_args(p, x, w, k_bytes, x_stride, w_stride), sms, st);
   p.k_blocks = static_cast<int>((k_bytes + 127) / 128);
+  p.wait_limit_us = hook_wait_limit_us.load(std::memory_order_relaxed);
+  p.withhold = hook_withhold.load(std::memory_order_relaxed);
   const DensePlan pl = plan_dense<KIND>(p.M, p.N, p.k_blocks, sms);
   const WarpsPlan pw = plan_warps<KIND>(p.M, p.N, k_bytes, sms);
   if (KIND == KIND_I8) {
@@ -427,8 +431,6 @@ moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_byt
   if (pw.cost < pl.cost) return run_warps<KIND>(pw, few_args(p, x, w, k_bytes, x_stride, w_stride), st);
   p.splits = pl.splits;
   p.tile_rows = pl.tile_rows;
-  p.wait_limit_us = hook_wait_limit_us.load(std::memory_order_relaxed);
-  p.withhold = hook_withhold.load(std::memory_order_relaxed);
   CUtensorMap tx, tw;
   if (!make_dense_map(&tx, x, k_bytes, p.M, x_stride, p.tile_rows) ||
       !make_dense_map(&tw, w, k_bytes, p.N, w_stride, pl.nt))

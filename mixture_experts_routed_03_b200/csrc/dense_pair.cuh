@@ -17,7 +17,12 @@
 // What bounds it: the tensor cores while a tile's K axis is long; the waves
 // of tiles over the 74 pairs when there are few.
 //
-// Tensor memory, dependents and waits as in dense.cuh.
+// Tensor memory and dependents as in dense.cuh.  Every wait is bounded; a wait
+// that runs out raises the CTA's abort flag, which its warps pass on to the other
+// CTA before the pair meets at the end.  Then the flags are final: if one is
+// raised, the status word gets MOE_ERR_TIMEOUT and the pair waits (bounded too)
+// for the copies and MMAs of both in flight before it meets again and gives shared
+// and tensor memory up.  Tiles that were finished before have been stored.
 #pragma once
 
 #include "dense.cuh"
@@ -41,6 +46,7 @@ struct PairArgs {
   int64_t out_stride;
   int vec;                             // rows of out are whole 16-byte pieces: stored by TMA
   int* status;
+  int wait_limit_us, withhold;         // as in DenseArgs
 };
 
 struct PairHeader {
@@ -48,7 +54,8 @@ struct PairHeader {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem;
-  alignas(16) volatile int abort_flag[4];
+  alignas(16) volatile int abort_flag[4];    // raised, wait limit (0: the default), raised by the other CTA
+  alignas(16) int64_t issued[2];             // stages loaded, by the end of the loading thread's part
   alignas(16) float ws[2][256], bias[2][256];
 };
 
@@ -102,6 +109,32 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Sets an int at an address of the cluster.
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Counts bytes that will not come as come.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
+}
+
+// After an abort, in the first CTA: waits for the copies of both, `mine` stages
+// of this CTA and `theirs` of the other, the last `ST` of them at most in flight.
+// A stage that only one CTA loaded has half of its bytes: armed for that half
+// here, where this CTA had not come to it, or with the other half counted off.
+template <int ST>
+__device__ __forceinline__ void drain_pair_copies(PairHeader* hdr, int64_t mine, int64_t theirs, uint32_t half) {
+  const int64_t all = mine > theirs ? mine : theirs;
+  for (int64_t i = all > ST ? all - ST : 0; i < all; ++i) {
+    uint64_t* bar = &hdr->full[i % ST];
+    if (i >= mine) mbar_arrive_expect_tx(bar, half);
+    else if (i >= theirs) mbar_complete_tx(bar, half);
+    drain_wait(bar, (i / ST) & 1, hdr->abort_flag);
+  }
 }
 
 // A warp's 32 x 32 outputs, row `lane` of them in v, to rows m0 .. m0 + 31 and
@@ -168,6 +201,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles = p.m_tiles * p.n_tiles;
+  // k blocks of this pair's tiles
+  const int64_t blocks = pair < tiles ? (static_cast<int64_t>(tiles - pair - 1) / pairs + 1) * p.k_blocks : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
@@ -180,7 +215,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
     }
     mbar_init(&hdr->drain, 1);
     abort_flag[0] = 0;
-    abort_flag[1] = 0;
+    abort_flag[1] = p.wait_limit_us;
+    abort_flag[2] = 0;
     fence_mbar_init();
   }
   if (warp == 8 && lane == 0) {
@@ -207,6 +243,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
       asm volatile("fence.proxy.async.global;" ::: "memory");
       int stage = 0;
       uint32_t phase = 0;
+      // all, or one less where a test withholds the last
+      const bool hold = (p.withhold == MOE_HOLD_LOAD && blockIdx.x == 0) ||
+                        (p.withhold == MOE_HOLD_LOAD_OF_SECOND && blockIdx.x == 1);
+      const int64_t loads = blocks - (hold ? 1 : 0);
       int64_t issued = 0;
       bool go = true;
       for (int t = pair; t < tiles && go; t += pairs) {
@@ -218,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
         int n = nt * NT + static_cast<int>(rank) * (NT / 2);
         if (n >= p.N) n = nt * NT;
         for (int kb = 0; kb < p.k_blocks; ++kb) {
-          go = mbar_wait(&hdr->empty[stage], phase ^ 1u, abort_flag, nullptr, 0);
+          go = issued < loads && mbar_wait(&hdr->empty[stage], phase ^ 1u, abort_flag, nullptr, 0);
           if (!go) break;
           uint8_t* sa = ring + stage * Cfg::kStageBytes;
           const uint32_t bar = mapa_rank(smem_u32(&hdr->full[stage]), 0);
@@ -232,14 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
           }
         }
       }
-      if (*abort_flag && rank == 0) {
-        // both CTAs' copies land before the shared memory is given up
-        for (int64_t i = issued > ST ? issued - ST : 0; i < issued; ++i) {
-          const unsigned long long t0 = globaltimer_ns();
-          while (!mbar_test(&hdr->full[i % ST], (i / ST) & 1))
-            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-        }
-      }
+      hdr->issued[0] = issued;
     }
   } else if (warp == 9) {
     if (rank == 0 && elect_one()) {
@@ -250,8 +283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
       int buf = 0;
       uint32_t buf_phase = 1;
       bool go = true;
-      // k blocks of this pair's tiles from here on
-      int64_t ahead = pair < tiles ? (static_cast<int64_t>(tiles - pair - 1) / pairs + 1) * p.k_blocks : 0;
+      int64_t ahead = blocks;                  // k blocks from here on
+      const bool hold = p.withhold == MOE_HOLD_SUM && pair == 0;
       for (int t = pair; t < tiles && go; t += pairs) {
         go = mbar_wait(&hdr->acc_empty[buf], buf_phase, abort_flag, nullptr, 0);
         if (!go) break;
@@ -272,15 +305,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
             phase ^= 1u;
           }
         }
-        mma_commit_pair(&hdr->acc_full[buf]);
+        if (!go) break;                        // a tile without all of its products is no tile
+        if (!hold || ahead > 0) mma_commit_pair(&hdr->acc_full[buf]);
         buf ^= 1;
         buf_phase ^= buf == 0;
-      }
-      if (*abort_flag) {
-        mma_commit_pair(&hdr->drain);
-        const unsigned long long t0 = globaltimer_ns();
-        while (!mbar_test(&hdr->drain, 0))
-          if (globaltimer_ns() - t0 > kWaitLimitNs) break;
       }
     }
   } else {
@@ -370,9 +398,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDenseThreads, 1)
     if (lane == 0) bulk_wait_done();
   }
   __syncwarp();
-  if (threadIdx.x == 0 && *abort_flag) record_error(p.status, MOE_ERR_TIMEOUT);
+  // whichever warp raised the flag tells the other CTA: once the pair has met, both know
+  if (lane == 0 && abort_flag[0]) st_cluster(mapa_rank(smem_u32(const_cast<int*>(abort_flag + 2)), rank ^ 1u), 1);
+  __syncwarp();
   tc_fence_before();
   cluster_sync_all();                  // neither CTA leaves while the other signals it
+  if (abort_flag[0] || abort_flag[2]) {
+    __syncwarp();
+    if (threadIdx.x == 0) record_error(p.status, MOE_ERR_TIMEOUT);
+    if (warp == 8 && rank == 0 && elect_one()) {
+      const uint4 theirs = ld_cluster16(mapa_rank(smem_u32(hdr->issued), 1));
+      drain_pair_copies<ST>(hdr, hdr->issued[0], static_cast<int64_t>(theirs.y) << 32 | theirs.x, Cfg::kStageBytes);
+    }
+    if (warp == 9 && elect_one()) {
+      if (rank == 0) mma_commit_pair(&hdr->drain);     // the thread that issued the MMAs
+      drain_wait(&hdr->drain, 0, abort_flag);
+    }
+    __syncwarp();
+    cluster_sync_all();
+  }
   tc_fence_after();
   __syncwarp();
   if (warp == 9)

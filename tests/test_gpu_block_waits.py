@@ -77,6 +77,23 @@ def test_tile_that_waits_in_vain_is_not_stored(kind, M, N, K, hold):
     assert not (left[-1] == 7).all()           # others are
 
 
+# CTA pairs: more tiles than pairs and fewer, every tile width; the second CTA's load is the one that its pair's first waits for
+PAIRS = [(4096, 4096, 512), (2500, 2500, 144), (9473, 257, 130), (5000, 700, 400), (2048, 4096, 512), (16384, 4096, 1024)]
+
+
+@pytest.mark.parametrize("M,N,K", PAIRS)
+@pytest.mark.parametrize("hold", ["load", "sum", "load_of_second"])
+def test_pair_that_waits_in_vain(M, N, K, hold):
+    K = -(-K // 16) * 16
+    left = _run_out("int8", M, N, K, hold)
+    assert (left == 7).any() and not (left == 7).all()      # the pair's last tile at least; the others' are stored
+
+
+@pytest.mark.parametrize("kind,M,N,K", [("router", 4736, 281, 6912), ("int8", 274, 665, 5040)])
+def test_second_cta_of_a_cluster_that_waits_in_vain(kind, M, N, K):
+    assert (_run_out(kind, M, N, K, "load_of_second")[0, :32] == 7).all()
+
+
 def test_hooks_are_part_of_a_captured_call_and_of_no_other():
     run, out, status, right = _call("router", 996, 132, 6144)
     run()
