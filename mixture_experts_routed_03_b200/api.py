@@ -133,19 +133,27 @@ _address = {}     # entry point -> address, for it
 def _short(name):
     """(call, address) of an entry point that is called through the extension
     of csrc/binding.c: ctypes marshals ten arguments in two microseconds, as
-    long as the kernels of a few tokens take."""
+    long as the kernels of a few tokens take.  Where the extension was not
+    built, ctypes makes the same calls."""
     global _call
     if _call is None:
         L = lib()
         try:
-            from . import _binding
-        except ImportError as e:
-            raise RuntimeError("the _binding extension is missing: run __graft_entry__.build() "
-                               "(or python -m mixture_experts_routed_03_b200.build)") from e
+            from ._binding import call
+        except ImportError:
+            call = _ctypes_call
         for n in ("moe_rmsnorm_quantize", "moe_router_logits", "moe_matmul_int8"):
             _address[n] = ctypes.cast(getattr(L, n), ctypes.c_void_p).value
-        _call = _binding.call
+        _call = call
     return _call, _address[name]
+
+
+def _ctypes_call(address, *args):
+    """csrc/binding.c's call(address, *args), by ctypes."""
+    if len(args) not in (6, 9, 10):
+        raise TypeError("call() makes calls of 6, 9 or 10 arguments")
+    fn = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * len(args))(address)
+    return fn(*[a if a is None or isinstance(a, int) else a.data_ptr() for a in args])
 
 
 def lib():

@@ -2,9 +2,11 @@
 before anything is launched (the pointers are never dereferenced).  CPU only."""
 
 import ctypes
+import importlib.machinery
 import os
 import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -236,6 +238,40 @@ def test_binding_function_checks_its_own_arguments(lib):
     for args in ((), (at,), (at, 0), (at,) + (0,) * 13):
         with pytest.raises(TypeError):
             call(*args)
+
+
+# ------------------------------------------------------------------ without the extension
+
+@pytest.fixture
+def without_extension(lib, monkeypatch):
+    """api as it is where csrc/binding.c was not built."""
+    monkeypatch.setitem(sys.modules, "mixture_experts_routed_03_b200._binding", None)
+    monkeypatch.setattr(api, "_call", None)
+    assert api._short("moe_router_logits")[0] is api._ctypes_call
+
+
+def test_calls_without_the_extension(without_extension, lib):
+    test_binding_takes_tensors_integers_and_none(lib)
+    test_binding_raises_the_librarys_errors(lib)
+    test_binding_refuses_what_is_no_problem_or_pointer(lib)
+    test_binding_function_checks_its_own_arguments(lib)
+
+
+def test_extension_bears_the_interpreters_tag_and_is_the_one_loaded(lib):
+    from mixture_experts_routed_03_b200 import _binding
+    assert os.path.basename(build.BINDING_OUT) == "_binding" + importlib.machinery.EXTENSION_SUFFIXES[0]
+    assert _binding.__file__ == build.BINDING_OUT
+
+
+@pytest.mark.parametrize("cc", ["missing", "failing"])
+def test_build_without_a_c_compiler_or_python_headers_warns(cc, tmp_path, monkeypatch):
+    monkeypatch.setattr(build, "BINDING_OUT", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(build, "HERE", str(tmp_path))
+    monkeypatch.setattr(build.shutil, "which", lambda name: None if cc == "missing" else "false")
+    (tmp_path / "_binding.so").write_text("built from an older source")
+    with pytest.warns(UserWarning, match="not built"):
+        build._build_binding()
+    assert not (tmp_path / "_binding.so").exists()       # nothing stale is left to be loaded
 
 
 # ------------------------------------------------------------------ the products' test hook
