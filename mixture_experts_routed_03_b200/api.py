@@ -219,9 +219,10 @@ def _ptr(t):
 
 def _stream(s):
     if s is None:
-        # the raw handle alone: a Stream object costs a microsecond a call
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the raw handle alone, where this torch gives it: a Stream object costs a microsecond a call
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream

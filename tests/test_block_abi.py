@@ -7,6 +7,7 @@ import os
 import shutil
 import subprocess
 import sys
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -272,6 +273,18 @@ def test_build_without_a_c_compiler_or_python_headers_warns(cc, tmp_path, monkey
     with pytest.warns(UserWarning, match="not built"):
         build._build_binding()
     assert not (tmp_path / "_binding.so").exists()       # nothing stale is left to be loaded
+
+
+@pytest.mark.parametrize("private", [True, False])
+def test_current_stream_with_and_without_torchs_private_call(private, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: SimpleNamespace(cuda_stream=42))
+    if private:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 40 + device, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert api._stream(None) == (43 if private else 42)
+    assert api._stream(7) == 7 and api._stream(SimpleNamespace(cuda_stream=8)) == 8
 
 
 # ------------------------------------------------------------------ the products' test hook
