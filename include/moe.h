@@ -492,6 +492,25 @@ moe_status_t moe_matmul_int8(const moe_int8_matmul_t* problem, const int8_t* x, 
                              const int8_t* w, const float* w_scale, const float* bias, void* out,
                              int32_t* device_status, void* stream);
 
+/* The kernel, tile and K split that a product of these sizes takes on the
+ * current device (of 148 SMs where there is none); host only, for inspection
+ * and tests.  The integer product where is_int8 is 1, else the router's. */
+typedef enum {
+  MOE_PRODUCT_FEW = 0,     /* dot products, a warp or more to an output column */
+  MOE_PRODUCT_WARPS = 1,   /* warp-level MMAs on registers */
+  MOE_PRODUCT_TILES = 2,   /* tcgen05, one CTA or cluster to a tile */
+  MOE_PRODUCT_PAIRS = 3    /* tcgen05 on CTA pairs, persistent */
+} moe_product_kernel_t;
+typedef struct {
+  int32_t kernel;          /* moe_product_kernel_t */
+  int32_t rows, cols;      /* of the output tile of a block, cluster or pair */
+  int32_t splits;          /* parts that K is split into: warps of a block (FEW) or CTAs of a cluster */
+  int32_t stage_blocks;    /* 128-byte blocks of K in a pipeline stage (TILES, PAIRS), else 0 */
+  float estimate_us;       /* the time that the choice goes by; 0 where there is none (FEW) */
+} moe_product_plan_t;
+moe_status_t moe_get_product_plan(int32_t is_int8, int64_t num_tokens, int32_t in_features, int32_t out_features,
+                                  moe_product_plan_t* plan);
+
 /* Test hook of the products' failure detection, on the host: for calls of
  * moe_router_logits and moe_matmul_int8 enqueued (or captured) by this process
  * from now on, a wait limit in microseconds for every bounded wait (0: the

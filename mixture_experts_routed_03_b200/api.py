@@ -41,7 +41,8 @@ EXPORTS = (
     "moe_fused", "moe_read_status", "moe_status_string", "moe_timing_enable", "moe_timing_read",
     "moe_permute_noalloc", "moe_get_tile_regime", "moe_get_workspace_offsets",
     "moe_workspace_test_hooks", "moe_quantize_nvfp4_rowwise",
-    "moe_rmsnorm_quantize", "moe_router_logits", "moe_matmul_int8", "moe_product_test_hooks",
+    "moe_rmsnorm_quantize", "moe_router_logits", "moe_matmul_int8", "moe_get_product_plan",
+    "moe_product_test_hooks",
 )
 
 SLOTS = ("route", "permute", "gather", "gemm1", "zero", "gemm2", "finalize", "combine", "fused")
@@ -116,6 +117,17 @@ class Int8Problem(ctypes.Structure):
     ]
 
 
+class ProductPlan(ctypes.Structure):
+    _fields_ = [
+        ("kernel", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("splits", ctypes.c_int32),
+        ("stage_blocks", ctypes.c_int32),
+        ("estimate_us", ctypes.c_float),
+    ]
+
+
 WS_OFFSET_FIELDS = ("status", "topk_idx", "topk_weights", "expert_counts", "expert_start_indices",
                     "src_info", "slot_to_row", "expert_ids", "num_active", "a_scale_offsets",
                     "tile_offsets", "intermediate", "intermediate_scales", "scale_rows", "accumulator")
@@ -175,6 +187,7 @@ def lib():
             "moe_rmsnorm_quantize": [ctypes.POINTER(NormProblem)] + [vp] * 9,
             "moe_router_logits": [P, vp, vp, vp, vp, vp],
             "moe_matmul_int8": [ctypes.POINTER(Int8Problem)] + [vp] * 8,
+            "moe_get_product_plan": [i32, ctypes.c_int64, i32, i32, ctypes.POINTER(ProductPlan)],
             "moe_product_test_hooks": [i32, i32],
             "moe_prepare_weights": [P, ctypes.POINTER(Weights), vp, vp, vp],
             "moe_get_prepared_weights_size": [P, ctypes.POINTER(sz), ctypes.POINTER(sz)],
@@ -240,6 +253,7 @@ def _check(fn, code):
 
 TILE_REGIMES = {"auto": 0, "large_m": 1, "small_m": 2}
 ACTIVATIONS = {"swiglu": 0, "swigluoai": 1}
+PRODUCT_KERNELS = ("few", "warps", "tiles", "pairs")
 PRODUCT_HOLDS = {"nothing": 0, "load": 1, "sum": 2, "load_of_second": 3}
 NORM_FORMATS = {"bf16": 0, "fp8": 1, "mxfp8": 3, "fp8_tensor": 4, "int8": 5}
 
@@ -396,6 +410,15 @@ def matmul_int8(prob, x, x_scale, w, w_scale, out, device_status, bias=None, str
     code = call(at, ctypes.addressof(prob), x, x_scale, w, w_scale, bias, out, device_status, _stream(stream))
     if code:
         raise MoEError("moe_matmul_int8", code)
+
+
+def product_plan(is_int8, num_tokens, in_features, out_features):
+    """The ProductPlan of matmul_int8 or router_logits at these sizes (host
+    only); its kernel is a PRODUCT_KERNELS index."""
+    plan = ProductPlan()
+    _check("moe_get_product_plan", lib().moe_get_product_plan(int(bool(is_int8)), int(num_tokens), int(in_features),
+                                                              int(out_features), ctypes.byref(plan)))
+    return plan
 
 
 def product_test_hooks(wait_limit_us=0, hold="nothing"):

@@ -145,7 +145,6 @@ bool make_out_map(CUtensorMap* m, void* base, bool fp32, uint64_t cols, uint64_t
 }
 
 struct DensePlan {
-  int pair;         // the CTA-pair kernel, nt columns wide; else dense_kernel:
   int nt;           // output columns per tile
   int splits;       // CTAs that share a tile's K axis
   int tile_rows;    // output rows per tile
@@ -179,7 +178,7 @@ int dense_stage_blocks(int kind, int rows, int nt, int splits, int64_t ctas, int
 template <int KIND>
 DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
   constexpr int kWidest = 256;
-  DensePlan best{0, kWidest, 1, 128, 1e300};
+  DensePlan best{kWidest, 1, 128, 1e300};
   for (int nt = kWidest; nt >= kDenseNarrowest<KIND>; nt /= 2) {
     const int64_t n_tiles = (N + nt - 1) / nt;
     for (int s = 1; s <= 8; s *= 2) {
@@ -204,7 +203,7 @@ DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
                                       (s > 1 ? 1200.0 * std::sqrt(static_cast<double>(s)) : 0.0));
       const double memory = 3000.0 + static_cast<double>(M + N) * k_blocks * 128.0 / 6000.0;
       if (cost < memory) cost = memory;
-      if (cost < best.cost) best = {0, nt, s, static_cast<int>(rows), cost};
+      if (cost < best.cost) best = {nt, s, static_cast<int>(rows), cost};
     }
   }
   return best;
@@ -213,7 +212,7 @@ DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
 // The CTA-pair kernel's tile width, likewise: waves of tiles, each the slower
 // of its main loop and the epilogue of the tile before it.
 DensePlan plan_pair(int64_t M, int N, int k_blocks, int sms) {
-  DensePlan best{1, 256, 1, 256, 1e300};
+  DensePlan best{256, 1, 256, 1e300};
   if (sms < 2) return best;
   for (int nt = 256; nt >= 128; nt -= 64) {
     const int64_t tiles = (M + 255) / 256 * ((N + nt - 1) / nt);
@@ -221,16 +220,15 @@ DensePlan plan_pair(int64_t M, int N, int k_blocks, int sms) {
     // 200, 256 and 312 ns a k block were measured for 128, 192 and 256 columns
     const double main = k_blocks * (88.0 + 0.875 * nt), epilogue = 12.0 * nt;
     const double cost = 3100.0 + waves * (main > epilogue ? main : epilogue) + epilogue;
-    if (cost < best.cost) best = {1, nt, 1, 256, cost};
+    if (cost < best.cost) best = {nt, 1, 256, cost};
   }
   return best;
 }
 
 template <int KIND, int NT>
-cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap& tw, int sms, cudaStream_t st) {
+cudaError_t launch_dense(DenseArgs& p, const CUtensorMap& tx, const CUtensorMap& tw, cudaStream_t st) {
   p.n_tiles = (p.N + NT - 1) / NT;
   const int64_t grid = (p.M + p.tile_rows - 1) / p.tile_rows * p.n_tiles * p.splits;
-  p.stage_blocks = dense_stage_blocks(KIND, p.tile_rows, NT, p.splits, grid, sms);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const int block = (p.tile_rows + NT) * 128, stage = block * p.stage_blocks;
   const int fixed = dense_fixed_bytes(block);
@@ -307,13 +305,20 @@ cudaError_t launch_warps(const FewArgs& a, cudaStream_t st) {
                   a, n_tiles);
 }
 
-template <int KIND, int MB, int R, int D>
-cudaError_t launch_few(const FewArgs& a, int sms, cudaStream_t st) {
-  // warps that share a row: as many as it takes to give every SM two blocks,
-  // while each still has a full load of its own
+constexpr int kFewRows = 2;   // rows of w per warp
+
+// Warps that share a row: as many as it takes to give every SM two blocks,
+// while each still has a full load of its own.
+int few_split(int N, int64_t k_bytes, int sms) {
   int wk = 1;
-  const int rows8 = (a.N + R * kFewWarps - 1) / (R * kFewWarps);
-  while (wk < kFewWarps && rows8 * wk < 2 * sms && a.k_bytes >= 1024 * wk) wk *= 2;
+  const int rows8 = (N + kFewRows * kFewWarps - 1) / (kFewRows * kFewWarps);
+  while (wk < kFewWarps && rows8 * wk < 2 * sms && k_bytes >= 1024 * wk) wk *= 2;
+  return wk;
+}
+
+template <int KIND, int MB>
+cudaError_t launch_few(const FewArgs& a, int wk, cudaStream_t st) {
+  constexpr int R = kFewRows, D = 4;
   const int per_block = kFewWarps / wk * R;
   const int grid = (a.N + per_block - 1) / per_block;
   switch (wk) {
@@ -344,11 +349,11 @@ FewArgs few_args(const DenseArgs& p, const void* x, const void* w, int64_t k_byt
 }
 
 template <int KIND>
-moe_status_t run_few(const FewArgs& a, int sms, cudaStream_t st) {
+moe_status_t run_few(const moe_product_plan_t& pl, const FewArgs& a, cudaStream_t st) {
   cudaError_t e;
-  if (a.M == 1) e = launch_few<KIND, 1, 2, 4>(a, sms, st);
-  else if (a.M == 2 || KIND == KIND_I8) e = launch_few<KIND, 2, 2, 4>(a, sms, st);
-  else e = launch_few<KIND_BF16, 4, 2, 4>(a, sms, st);
+  if (pl.rows == 1) e = launch_few<KIND, 1>(a, pl.splits, st);
+  else if (pl.rows == 2 || KIND == KIND_I8) e = launch_few<KIND, 2>(a, pl.splits, st);
+  else e = launch_few<KIND_BF16, 4>(a, pl.splits, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -363,8 +368,8 @@ cudaError_t run_warps_split(int splits, const FewArgs& a, cudaStream_t st) {
 }
 
 template <int KIND>
-moe_status_t run_warps(const WarpsPlan& pl, const FewArgs& a, cudaStream_t st) {
-  const cudaError_t e = pl.xt == 1 ? run_warps_split<KIND, 1>(pl.splits, a, st)
+moe_status_t run_warps(const moe_product_plan_t& pl, const FewArgs& a, cudaStream_t st) {
+  const cudaError_t e = pl.rows == 8 ? run_warps_split<KIND, 1>(pl.splits, a, st)
                                    : run_warps_split<KIND, kWarpsTall<KIND>>(pl.splits, a, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -412,35 +417,54 @@ moe_status_t run_pair(const DenseArgs& p, int nt, const void* x, const void* w, 
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// Kernel, tile and split of out [M, N] = x [M, K bytes] w [N, K bytes]^T, M at least 1.
+template <int KIND>
+moe_product_plan_t plan_product(int64_t M, int N, int64_t k_bytes, int sms) {
+  if (M <= kFewMaxM<KIND>) {
+    const int wk = few_split(N, k_bytes, sms);
+    const int rows = M <= 2 ? static_cast<int>(M) : 4;
+    return {MOE_PRODUCT_FEW, rows, kFewWarps / wk * kFewRows, wk, 0, 0.0f};
+  }
+  const int k_blocks = static_cast<int>((k_bytes + 127) / 128);
+  const DensePlan pl = plan_dense<KIND>(M, N, k_blocks, sms);
+  const WarpsPlan pw = plan_warps<KIND>(M, N, k_bytes, sms);
+  if (KIND == KIND_I8) {
+    const DensePlan pp = plan_pair(M, N, k_blocks, sms);
+    if (pp.cost < pl.cost && pp.cost < pw.cost)
+      return {MOE_PRODUCT_PAIRS, pp.tile_rows, pp.nt, 1, 1, static_cast<float>(pp.cost * 1e-3)};
+  }
+  if (pw.cost < pl.cost)
+    return {MOE_PRODUCT_WARPS, 8 * pw.xt, 16, pw.splits, 0, static_cast<float>(pw.cost * 1e-3)};
+  const int64_t ctas = (M + pl.tile_rows - 1) / pl.tile_rows * ((N + pl.nt - 1) / pl.nt) * pl.splits;
+  return {MOE_PRODUCT_TILES, pl.tile_rows, pl.nt, pl.splits,
+          dense_stage_blocks(KIND, pl.tile_rows, pl.nt, pl.splits, ctas, sms), static_cast<float>(pl.cost * 1e-3)};
+}
+
 // out [M, N] = x [M, K bytes] w [N, K bytes]^T; strides in bytes.
 template <int KIND>
 moe_status_t run_dense(DenseArgs& p, const void* x, const void* w, int64_t k_bytes, int64_t x_stride, int64_t w_stride,
                        cudaStream_t st) {
   const int sms = sm_count();
-  if (p.M <= kFewMaxM<KIND>) return run_few<KIND>(few_args(p, x, w, k_bytes, x_stride, w_stride), sms, st);
+  const moe_product_plan_t pl = plan_product<KIND>(p.M, p.N, k_bytes, sms);
+  if (pl.kernel == MOE_PRODUCT_FEW) return run_few<KIND>(pl, few_args(p, x, w, k_bytes, x_stride, w_stride), st);
+  if (pl.kernel == MOE_PRODUCT_WARPS) return run_warps<KIND>(pl, few_args(p, x, w, k_bytes, x_stride, w_stride), st);
   p.k_blocks = static_cast<int>((k_bytes + 127) / 128);
   p.wait_limit_us = hook_wait_limit_us.load(std::memory_order_relaxed);
   p.withhold = hook_withhold.load(std::memory_order_relaxed);
-  const DensePlan pl = plan_dense<KIND>(p.M, p.N, p.k_blocks, sms);
-  const WarpsPlan pw = plan_warps<KIND>(p.M, p.N, k_bytes, sms);
-  if (KIND == KIND_I8) {
-    const DensePlan pp = plan_pair(p.M, p.N, p.k_blocks, sms);
-    if (pp.cost < pl.cost && pp.cost < pw.cost)
-      return run_pair(p, pp.nt, x, w, k_bytes, x_stride, w_stride, sms, st);
-  }
-  if (pw.cost < pl.cost) return run_warps<KIND>(pw, few_args(p, x, w, k_bytes, x_stride, w_stride), st);
+  if (pl.kernel == MOE_PRODUCT_PAIRS) return run_pair(p, pl.cols, x, w, k_bytes, x_stride, w_stride, sms, st);
   p.splits = pl.splits;
-  p.tile_rows = pl.tile_rows;
+  p.tile_rows = pl.rows;
+  p.stage_blocks = pl.stage_blocks;
   CUtensorMap tx, tw;
   if (!make_dense_map(&tx, x, k_bytes, p.M, x_stride, p.tile_rows) ||
-      !make_dense_map(&tw, w, k_bytes, p.N, w_stride, pl.nt))
+      !make_dense_map(&tw, w, k_bytes, p.N, w_stride, pl.cols))
     return MOE_ERR_CUDA;
   cudaError_t e;
-  switch (pl.nt) {
-    case 32: e = launch_dense<KIND, kDenseNarrowest<KIND>>(p, tx, tw, sms, st); break;   // integers alone
-    case 64: e = launch_dense<KIND, 64>(p, tx, tw, sms, st); break;
-    case 128: e = launch_dense<KIND, 128>(p, tx, tw, sms, st); break;
-    default: e = launch_dense<KIND, 256>(p, tx, tw, sms, st); break;
+  switch (pl.cols) {
+    case 32: e = launch_dense<KIND, kDenseNarrowest<KIND>>(p, tx, tw, st); break;   // integers alone
+    case 64: e = launch_dense<KIND, 64>(p, tx, tw, st); break;
+    case 128: e = launch_dense<KIND, 128>(p, tx, tw, st); break;
+    default: e = launch_dense<KIND, 256>(p, tx, tw, st); break;
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -614,6 +638,19 @@ moe_status_t moe_matmul_int8(const moe_int8_matmul_t* p, const int8_t* x, const 
   a.vec = aligned(out, 4 * ob) && os % 4 == 0;
   a.status = device_status;
   return run_dense<KIND_I8>(a, x, w, K, xs, ws, static_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_get_product_plan(int32_t is_int8, int64_t num_tokens, int32_t in_features, int32_t out_features,
+                                  moe_product_plan_t* plan) {
+  if (!plan || (is_int8 & ~1) || num_tokens < 1 || in_features < 1 || out_features < 1) return MOE_ERR_INVALID_ARG;
+  // as the calls themselves take them
+  if (num_tokens > kMaxRows || out_features > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (is_int8 ? in_features >= 131072 : in_features > 1 << 29 || out_features > 1024) return MOE_ERR_UNSUPPORTED;
+  if (!is_int8 && in_features % 256 != 0) return MOE_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  *plan = is_int8 ? plan_product<KIND_I8>(num_tokens, out_features, in_features, sms)
+                  : plan_product<KIND_BF16>(num_tokens, out_features, int64_t(2) * in_features, sms);
+  return MOE_OK;
 }
 
 moe_status_t moe_product_test_hooks(int32_t wait_limit_us, int32_t hold) {
