@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       abort_flag[0] = 0;
       abort_flag[1] = p.wait_limit_us;
       fence_mbar_init();
+      fence_async_smem();                      // the first copies count on barriers that no block barrier stands behind
       pdl_wait();
       asm volatile("fence.proxy.async.global;" ::: "memory");
       for (int s = 0; s < early; ++s) load(s, kb0 + s * p.stage_blocks);
