@@ -451,7 +451,9 @@ typedef struct {
  * throughout, a block whose amax is not finite NaN in the block: scales NaN (MXFP8: 255), E4M3
  * codes NaN, integer codes 0.  Every pointer is 16-byte aligned, FP32 scales
  * 4-byte; outputs overlap neither inputs nor one another
- * (MOE_ERR_INVALID_ARG). */
+ * (MOE_ERR_INVALID_ARG).  An argument covers all addresses from its first
+ * element to its last, what lies between its rows included: slices of the
+ * columns of one buffer overlap. */
 moe_status_t moe_rmsnorm_quantize(const moe_norm_t* problem, const void* x, const void* residual_in,
                                   const void* weight, const float* static_scale, void* residual_out,
                                   void* norm_out, void* codes, void* scales, void* stream);
@@ -487,7 +489,7 @@ typedef struct {
  * is exact; it is rounded to FP32, multiplied by x_scale, then by w_scale,
  * and the bias is added, each in FP32; BF16 output rounds once more.
  * device_status as in moe_router_logits.  out overlaps no input
- * (MOE_ERR_INVALID_ARG). */
+ * (MOE_ERR_INVALID_ARG; addresses as in moe_rmsnorm_quantize). */
 moe_status_t moe_matmul_int8(const moe_int8_matmul_t* problem, const int8_t* x, const float* x_scale,
                              const int8_t* w, const float* w_scale, const float* bias, void* out,
                              int32_t* device_status, void* stream);

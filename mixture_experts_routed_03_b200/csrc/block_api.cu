@@ -81,7 +81,8 @@ cudaError_t launch_norm_rows(NormArgs a, int64_t M, int threads, cudaStream_t st
 //   else two, which halves the threads that share a row's reductions, five
 //     blocks an SM (4096 x 2048: 11.8 us against 12.4; 16384 x 4096, FP32
 //     residual: 139 against 146, both without the requests to L2), while a
-//     block can hold the row;
+//     block can hold the row; with 512 threads and three blocks an SM, for
+//     4352 to 8192 columns, that leaves 40 registers, and 40 to 60 bytes spill;
 //   above 16384 columns four.
 template <int FMT, int RES>
 cudaError_t launch_norm(const NormArgs& a, int64_t M, cudaStream_t st) {
@@ -171,10 +172,15 @@ int dense_stage_blocks(int kind, int rows, int nt, int splits, int64_t ctas, int
 
 // Tile and K split of dense_kernel by estimated time: whole waves of CTAs, one
 // an SM, each its share of the k blocks at the slowest of issue, loads and MMAs,
-// plus what a tile costs besides.  The constants are a fit to timings of 32
-// sizes, from 1 x 60 x 2048 to 16384 x 128 x 8192 bytes, at every width and
-// split.  (256 columns in BF16: 16384 x 256 x 7168 66 us, 98 in two tiles of 128;
-// 1000 x 256 x 7168 12.9 and 15.5.)
+// plus what a tile costs besides.  The constants were fitted to timings of 32
+// sizes made with up to two CTAs an SM and BF16 tiles of at most 128 columns.
+// Against timings of today's kernel, 23 sizes in BF16 (64 x 256 x 7168 to 16384 x
+// 512 x 4096) and 14 in integers (16 x 4096 x 7168 to 2048 x 1536 x 4096) at every
+// width and split that is considered: estimates 16 and 15 % off (rms), those of
+// 256 columns in BF16 too short (16384 x 256 x 7168: 49 us, 67 measured); the
+// choice is the best one at 18 of 23 and 10 of 14, 1.2 and 3.0 % slower than it on
+// average, 13 and 15 % at most.  (256 columns against 128: 16384 x 256 x 7168 67 and
+// 104 us, 1000 x 256 x 7168 13.1 and 15.1.)
 template <int KIND>
 DensePlan plan_dense(int64_t M, int N, int k_blocks, int sms) {
   constexpr int kWidest = 256;

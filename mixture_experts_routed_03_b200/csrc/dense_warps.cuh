@@ -16,9 +16,10 @@
 // exact too; after 512 the sum goes on in 32-bit integers.
 //
 // What bounds it: up to some hundred rows latency, then that w is read again
-// for every 8 XT rows of x and x for every 16 of w, which grows with M N; of
-// integers the conversions, five instructions for four codes.  Then the tcgen05
-// tiles of dense.cuh are faster.  BF16, H = 7168, 256 experts, against those: 9
+// for every 8 XT rows of x and x for every 16 of w, which grows with M N.  Then
+// the tcgen05 tiles of dense.cuh are faster.  The integers' conversions, five
+// instructions for four codes, are not it: at 4 x 2048 x 2048 an SM issues in 16 %
+// of its cycles and waits for loads.  BF16, H = 7168, 256 experts, against those: 9
 // rows 3.4 us (tiles 6.8), 64 rows 5.1 (7.7), 128 rows 6.3 (7.8), 256 rows 8.3
 // (10.4), 777 rows 26 (11.8); 64 x 60 x 2048: 2.4 (5.0).  Integers: 4 x 2048 x
 // 2048 3.6 us (5.3), 16 rows 4.1 (5.5), 32 rows 4.9 (5.8); 4 x 512 x 1024 2.1

@@ -19,8 +19,10 @@
 // 30 (8-bit codes) or 19 (BF16) instructions an element.  Against the first, a
 // block asks L2 for the row that a later one will read; against the second, two
 // columns go through one instruction (f32x2) where FP32 allows it, 39 -> 33.
-// 16384 x 4096, FP32 residual, FP8: 131 us of 135 at the copy rate (some of it
-// is still in L2); 4096 x 7168, BF16 residual, FP8: 46 of 41.
+// 16384 x 4096, FP32 residual, FP8: 129 us, where its bytes take 135 at the copy
+// rate: DRAM carries 88 % of them (382 of 436 MB at 8192 x 4096, 67 us: 5.7 TB/s),
+// the rest stays in L2.  4096 x 7168, BF16 residual, FP8: 46 us of 41, issuing in
+// 64 % of the cycles.
 //
 // Roundings.  A code changes where its value crosses the midpoint of two, so
 // the value is kept to about one FP32 rounding: the warps' FP32 sums of
