@@ -102,17 +102,17 @@ def _code_only(text):
 
 
 def kernel_sources_sha():
-    """SHA-256 over the code (comments removed) of the CUDA sources and the C
-    header: identifies the kernels a stored ncu traffic figure was measured
-    on; any code change drops the figure."""
+    """SHA-256 over the code (comments removed) of the layer's translation unit
+    and every header it includes, the C header among them: identifies the
+    kernels a stored ncu traffic figure was measured on.  A change to their
+    code drops the figure, one to other operators' kernels does not."""
     import hashlib
+    from mixture_experts_routed_03_b200 import build
     h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "mixture_experts_routed_03_b200", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name.endswith((".cu", ".cuh", ".h")):
-            h.update(name.encode())
-            h.update(_code_only(open(os.path.join(csrc, name)).read()).encode())
-    h.update(_code_only(open(os.path.join(ROOT, "include", "moe.h")).read()).encode())
+    for path in sorted(build._deps("moe_api.cu"), key=os.path.basename):
+        h.update(os.path.basename(path).encode())
+        with open(path) as f:
+            h.update(_code_only(f.read()).encode())
     return h.hexdigest()[:16]
 
 
